@@ -19,6 +19,7 @@ __all__ = [
     "km_update", "km_update_next", "km_update_partial", "km_finalize", "km_init_grid1d", "km_fit",
     "km_fit_host",
     "km_device_error", "km_assign_uses_tensor_cores", "workspace",
+    "km_pack4", "km_matvec4", "km_lookup", "km_lookup_grad", "km_xent", "km_xent_grad",
 ]
 
 KM_OP_ASSIGN, KM_OP_UPDATE, KM_OP_FIT, KM_OP_FIT_HOST = 0, 1, 2, 3
@@ -73,6 +74,15 @@ def _load():
         "km_split_dead": ([P, P, P, F, I64, I64, I64, P, P, P, P], I),
         "km_encode1d": ([P, I, I64, I64, P, I64, P, P], I),
         "km_init_kmeanspp1d": ([P, I, P, I64, I64, I64, P, P, P, P], I),
+        "km_pack4": ([P, I64, I64, P, P], I),
+        "km_matvec4": ([P, I, I64, P, P, I64, I64, I64, P, I64, P, P], I),
+        "km_lookup": ([P, I, P, I64, I64, I64, I64, F, P, P], I),
+        "km_lookup_grad_workspace_size": ([I64, I64, I64, I64], SZ),
+        "km_lookup_grad": ([P, I, P, I64, I64, I64, I64, F, P, I, I, P, SZ, P], I),
+        "km_xent_workspace_size": ([I64, I64, I64, I64, I], SZ),
+        "km_xent": ([P, I, P, P, I64, I64, I64, I64, F, P, P, P, SZ, P], I),
+        "km_xent_grad_workspace_size": ([I64, I64, I64, I64, I], SZ),
+        "km_xent_grad": ([P, I, P, P, P, P, I64, I64, I64, I64, F, P, P, P, SZ, P], I),
         "km_fit_stream": ([P, I, P, I64, I64, I64, I64, P, I, I64, P, P, SZ, P], I),
     }
     for name, (args, res) in sig.items():
@@ -394,6 +404,185 @@ def km_init_kmeanspp1d(X, K, u, w=None, want_chosen=False, stream=None):
     _check("km_init_kmeanspp1d", _load().km_init_kmeanspp1d(
         _p(X), _dt(X.dtype), _p(w), B, N, K, _p(u), _p(C), _p(chosen), _s(stream)))
     return C, chosen
+
+
+def _dims(t, name, n):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {tuple(t.shape)}")
+
+
+def _on_gpu(t, name):
+    """The CUDA device that an operator's first argument lies on; all others must share it."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    _need(t, name)
+    return t.device
+
+
+class _launch_on:
+    """Makes `dev` the current device and `stream` (a torch stream, a raw cudaStream_t or None for
+    the device's current stream) the current stream, so that outputs and workspaces allocated
+    inside belong to the stream that the kernels run on."""
+
+    def __init__(self, dev, stream):
+        if stream is None:
+            self._s = torch.cuda.current_stream(dev)
+        elif hasattr(stream, "cuda_stream"):
+            self._s = stream
+        elif int(stream) == 0:
+            self._s = torch.cuda.default_stream(dev)
+        else:
+            self._s = torch.cuda.ExternalStream(int(stream), device=dev)
+        if self._s.device != dev:
+            raise ValueError(f"the stream belongs to {self._s.device}, the tensors to {dev}")
+        self._dev, self._ctx = torch.cuda.device(dev), torch.cuda.stream(self._s)
+
+    def __enter__(self):
+        self._dev.__enter__()
+        self._ctx.__enter__()
+        return ctypes.c_void_p(self._s.cuda_stream)
+
+    def __exit__(self, *exc):
+        self._ctx.__exit__(*exc)
+        self._dev.__exit__(*exc)
+
+
+def _scratch(ws, nbytes, dev):
+    if ws is None:
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+    _need(ws, "ws", torch.uint8, None, dev)
+    return ws
+
+
+def km_pack4(codes, packed=None, stream=None):
+    """4-bit packing of codes [R,N] uint8 (values below 16, as km_encode1d writes them with
+    K <= 16). Returns packed [R, 16 * ceil(N / 32)] uint8."""
+    dev = _on_gpu(codes, "codes")
+    _dims(codes, "codes", 2)
+    _need(codes, "codes", torch.uint8)
+    R, N = codes.shape
+    with _launch_on(dev, stream) as s:
+        shape = (R, 16 * (-(-N // 32)))
+        packed = torch.empty(shape, dtype=torch.uint8, device=dev) if packed is None else packed
+        _need(packed, "packed", torch.uint8, shape, dev)
+        _check("km_pack4", _load().km_pack4(_p(codes), R, N, _p(packed), s))
+    return packed
+
+
+def km_matvec4(x, packed, C, scales=None, group=0, y=None, stream=None):
+    """Products of x [M,N] with weights held as 4-bit codes: y[m,r] = sum_n scales[r, n // group]
+    * C[r, code[r,n]] * x[m,n], the codebook values rounded to x's dtype, sums in fp32.
+    packed [R, 16 * ceil(N / 32)] (km_pack4), C [R,K] (or [R,K,1]) fp32 with K <= 16, scales
+    [R, ceil(N / group)] fp32 with group a multiple of 32, or None. Returns y [M,R] in x's dtype."""
+    dev = _on_gpu(x, "x")
+    _dims(x, "x", 2)
+    M, N = x.shape
+    if C.dim() == 3 and C.shape[2] == 1:
+        C = C.view(C.shape[0], C.shape[1])
+    _dims(C, "C", 2)
+    R, K = C.shape
+    _need(C, "C", torch.float32, None, dev)
+    _need(packed, "packed", torch.uint8, (R, 16 * (-(-N // 32))), dev)
+    if scales is not None:
+        if group < 1:
+            raise ValueError("scales need the group size")
+        _need(scales, "scales", torch.float32, (R, -(-N // group)), dev)
+    with _launch_on(dev, stream) as s:
+        y = torch.empty((M, R), dtype=x.dtype, device=dev) if y is None else y
+        _need(y, "y", x.dtype, (M, R), dev)
+        _check("km_matvec4", _load().km_matvec4(
+            _p(x), _dt(x.dtype), M, _p(packed), _p(C), R, N, K, _p(scales), group, _p(y), s))
+    return y
+
+
+def km_lookup(C, ids, scale=1.0, Y=None, stream=None):
+    """Table rows by id: Y[b,n] = scale * C[b, ids[b,n]], zero rows for ids outside [0,K).
+    C [B,K,d] of any supported dtype, ids [B,N] int32. Returns Y [B,N,d] in C's dtype."""
+    dev = _on_gpu(C, "C")
+    _dims(C, "C", 3)
+    _dims(ids, "ids", 2)
+    B, K, d = C.shape
+    N = ids.shape[1]
+    _need(ids, "ids", torch.int32, (B, N), dev)
+    with _launch_on(dev, stream) as s:
+        Y = torch.empty((B, N, d), dtype=C.dtype, device=dev) if Y is None else Y
+        _need(Y, "Y", C.dtype, (B, N, d), dev)
+        _check("km_lookup", _load().km_lookup(
+            _p(C), _dt(C.dtype), _p(ids), B, N, K, d, float(scale), _p(Y), s))
+    return Y
+
+
+def km_lookup_grad(dY, ids, K, scale=1.0, dC=None, out_dtype=None, accumulate=False, ws=None,
+                   stream=None):
+    """The table's gradient of km_lookup: dC[b,k] = scale * (sum of dY[b,n] over ids[b,n] == k),
+    in a fixed order. dY [B,N,d], ids [B,N] int32 (ids outside [0,K) are ignored). Returns dC
+    [B,K,d] in out_dtype (fp32 unless given; fp32 or dY's dtype); with accumulate the sums are
+    added to the given dC."""
+    dev = _on_gpu(dY, "dY")
+    _dims(dY, "dY", 3)
+    B, N, d = dY.shape
+    _need(ids, "ids", torch.int32, (B, N), dev)
+    if accumulate and dC is None:
+        raise ValueError("accumulate needs dC")
+    out_dtype = (torch.float32 if dC is None else dC.dtype) if out_dtype is None else out_dtype
+    with _launch_on(dev, stream) as s:
+        dC = torch.empty((B, K, d), dtype=out_dtype, device=dev) if dC is None else dC
+        _need(dC, "dC", out_dtype, (B, K, d), dev)
+        ws = _scratch(ws, _load().km_lookup_grad_workspace_size(B, N, K, d), dev)
+        _check("km_lookup_grad", _load().km_lookup_grad(
+            _p(dY), _dt(dY.dtype), _p(ids), B, N, K, d, float(scale), _p(dC), _dt(out_dtype),
+            int(bool(accumulate)), _p(ws), ws.numel(), s))
+    return dC
+
+
+def km_xent(X, C, ids, scale=1.0, loss=None, lse=None, ws=None, stream=None):
+    """Softmax cross entropy of X [B,N,d] against all rows of C [B,K,d] (same dtype), logits
+    scale * <x, c> never stored. ids [B,N] int32; ids outside [0,K) carry no label (loss 0).
+    Returns (loss, lse), both [B,N] fp32."""
+    dev = _on_gpu(X, "X")
+    _dims(X, "X", 3)
+    _dims(C, "C", 3)
+    B, N, d = X.shape
+    K = C.shape[1]
+    _need(C, "C", X.dtype, (B, K, d), dev)
+    _need(ids, "ids", torch.int32, (B, N), dev)
+    with _launch_on(dev, stream) as s:
+        loss = torch.empty((B, N), dtype=torch.float32, device=dev) if loss is None else loss
+        lse = torch.empty((B, N), dtype=torch.float32, device=dev) if lse is None else lse
+        _need(loss, "loss", torch.float32, (B, N), dev)
+        _need(lse, "lse", torch.float32, (B, N), dev)
+        ws = _scratch(ws, _load().km_xent_workspace_size(B, N, K, d, _dt(X.dtype)), dev)
+        _check("km_xent", _load().km_xent(
+            _p(X), _dt(X.dtype), _p(C), _p(ids), B, N, K, d, float(scale), _p(loss), _p(lse),
+            _p(ws), ws.numel(), s))
+    return loss, lse
+
+
+def km_xent_grad(X, C, ids, lse, g=None, scale=1.0, dX=None, dC=None, want_dX=True, want_dC=True,
+                 ws=None, stream=None):
+    """Gradients of sum_n g[b,n] * loss[b,n] of km_xent (lse as it returned it; g [B,N] fp32, None =
+    ones). Returns (dX [B,N,d], dC [B,K,d]) in X's dtype, None where not wanted."""
+    dev = _on_gpu(X, "X")
+    _dims(X, "X", 3)
+    _dims(C, "C", 3)
+    B, N, d = X.shape
+    K = C.shape[1]
+    _need(C, "C", X.dtype, (B, K, d), dev)
+    _need(ids, "ids", torch.int32, (B, N), dev)
+    _need(lse, "lse", torch.float32, (B, N), dev)
+    _need(g, "g", torch.float32, (B, N), dev)
+    with _launch_on(dev, stream) as s:
+        if want_dX and dX is None:
+            dX = torch.empty((B, N, d), dtype=X.dtype, device=dev)
+        if want_dC and dC is None:
+            dC = torch.empty((B, K, d), dtype=X.dtype, device=dev)
+        _need(dX, "dX", X.dtype, (B, N, d), dev)
+        _need(dC, "dC", X.dtype, (B, K, d), dev)
+        ws = _scratch(ws, _load().km_xent_grad_workspace_size(B, N, K, d, _dt(X.dtype)), dev)
+        _check("km_xent_grad", _load().km_xent_grad(
+            _p(X), _dt(X.dtype), _p(C), _p(ids), _p(lse), _p(g), B, N, K, d, float(scale),
+            _p(dX), _p(dC), _p(ws), ws.numel(), s))
+    return dX, dC
 
 
 def km_assign_uses_tensor_cores(X, Cx):

@@ -22,43 +22,14 @@
 #include "km_emeans.cuh"
 #include "km_fit1d.cuh"
 #include "km_fit_small.cuh"
+#include "km_host.h"
 #include "km_update.cuh"
 
 namespace {
 
 using km::Cvt;
 
-constexpr size_t kAlign = 256;
-constexpr int64_t kMaxIndex = (int64_t{1} << 31) - 1;
-constexpr int64_t kMaxD = int64_t{1} << 20;
-constexpr int kMaxGridY = 65535;
-
-inline size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-inline cudaStream_t S(void *s) { return reinterpret_cast<cudaStream_t>(s); }
-
-inline bool valid_dtype(km_dtype dt) { return dt == KM_F32 || dt == KM_F16 || dt == KM_BF16; }
-inline size_t dtype_size(km_dtype dt) { return dt == KM_F32 ? 4 : 2; }
-
-inline bool sizes_ok(int64_t B, int64_t N, int64_t K, int64_t d) {
-    return B >= 1 && N >= 1 && K >= 1 && d >= 1 && B <= kMaxIndex && N <= kMaxIndex &&
-           K <= kMaxIndex && d <= kMaxD && B * N <= (int64_t{1} << 40) &&
-           B * K <= (int64_t{1} << 40);
-}
-
 // ---------------------------------------------------------------- workspace layouts
-
-struct Carver {
-    uint8_t *base;
-    size_t off = 0;
-    explicit Carver(void *b) : base(static_cast<uint8_t *>(b)) {}
-    template <typename P> P *take(size_t bytes) {
-        P *p = base ? reinterpret_cast<P *>(base + off) : nullptr;
-        off += align_up(bytes);
-        return p;
-    }
-};
 
 inline bool tc_shape_ok(km_dtype dt, int64_t d) {
     return dt != KM_F32 && d % 8 == 0 && d >= 8 && d <= 256;
@@ -241,41 +212,6 @@ inline StreamWs carve_stream(Carver &c, int64_t B, int64_t K, int64_t d, km_dtyp
     c.off += u.off;   // the running sums/wsum live in this UpdateWs; the assignment scratch follows
     c.off += align_up(ws_assign(B, K, d, dt));
     return s;
-}
-
-// ---------------------------------------------------------------- device queries
-
-int num_sms() {
-    static int cache[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-    if (dev >= 0 && dev < 64 && cache[dev]) return cache[dev];
-    int n = 148;
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (dev >= 0 && dev < 64) cache[dev] = n;
-    return n;
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
-}
-
-inline km_status launch_status() {
-    return cudaGetLastError() == cudaSuccess ? KM_OK : KM_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------- kernel launchers

@@ -1,0 +1,278 @@
+// km_xent.cuh -- kernels of the softmax cross entropy of points against all K table rows.
+//
+//   z[n,k]  = scale * <x_n, c_k>            lse[n] = log sum_k exp(z[n,k])
+//   loss[n] = lse[n] - z[n, id_n]
+//   P[n,k]  = w_n (exp(z[n,k] - lse[n]) - [k == id_n])     w_n = g_n * scale, 0 without a label
+//   dX = P C          dC = P^T X
+//
+// The N x K logits are never stored. The loss reduces every tile of logits to one (maximum, sum of
+// exponentials) pair per row where the tile was computed, the same idea as the assignment's
+// running argmin, and joins the pairs of a row afterwards in tile order. The gradients recompute
+// the logits one piece of the table at a time into P (in the points' type) and multiply that.
+#pragma once
+
+#include "km_common.cuh"
+
+namespace km {
+namespace xe {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Mode { kLse = 0, kProb = 1, kOut = 2 };
+
+// What a product's tile does with its accumulators.
+struct Epi {
+    float scale;
+    // kLse: pairs[(b * tiles + tile) * M + row], zt[b * M + row] where the label's column falls
+    // in the tile
+    float2 *pairs;
+    float *zt;
+    const int32_t *ids;    // labels (kLse, kProb); the table piece starts at row k0 of K
+    int k0, K;
+    // kProb
+    const float *lse, *w;  // [B, M]
+    void *P;               // [B, M, ldp]
+    int64_t ldp;
+    // kOut: out = acc (fp32) + value / f, or the fp32 partial of one split of the reduction
+    const unsigned int *wmax;   // bits of max |w| (16-bit floats with a 5-bit exponent), or null
+    const float *acc;      // added, or null
+    float *out32;          // fp32 result or partials [split][B][M][N], or null
+    void *outT;            // result in the points' type, or null
+    int splits;
+};
+
+// P is held in the points' type. With fp16 its entries, probabilities times gradients, would fall
+// below the type's normal range, so they are scaled by a power of two that takes max |w| to
+// [2^14, 2^15) (|P| <= |w|, so nothing overflows) and the products are scaled back; both
+// scalings are exact.
+__device__ __forceinline__ float pow2_factor(const unsigned int *wmax, bool inverse) {
+    if (!wmax) return 1.f;
+    int e = 14 - (static_cast<int>(*wmax >> 23) - 127);
+    e = max(-100, min(100, e));
+    return __int_as_float((127 + (inverse ? -e : e)) << 23);
+}
+
+// ------------------------------------------------------------------ CUDA-core products
+
+// One operand of a product: element (row, k) of batch b at base + b * batch + row * row_s + k * k_s,
+// one of the two strides being 1.
+struct Operand {
+    const void *base;
+    int64_t batch, row_s, k_s;
+};
+
+constexpr int ST = 128;        // tile rows and columns
+constexpr int SK = 8;          // reduction step
+constexpr int kSimtThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void simt_stage(const Operand &o, int64_t b, int row0, int rows, int64_t k0, int64_t kend,
+                                           float (&dst)[SK][ST + 4]) {
+    const T *p = static_cast<const T *>(o.base) + b * o.batch;
+#pragma unroll
+    for (int i = 0; i < ST * SK / kSimtThreads; ++i) {
+        const int u = i * kSimtThreads + threadIdx.x;
+        const int k = o.k_s == 1 ? u % SK : u / ST, r = o.k_s == 1 ? u / SK : u % ST;
+        float v = 0.f;
+        if (row0 + r < rows && k0 + k < kend) v = Cvt<T>::to_f(p[(row0 + r) * o.row_s + (k0 + k) * o.k_s]);
+        dst[k][r] = v;
+    }
+}
+
+// D[b, m, n] = sum_k A[b, m, k] B[b, n, k]; 128 x 128 tiles, 8 x 8 accumulators per thread (four
+// 4 x 4 blocks 64 apart), operands staged as fp32. grid.x = tiles * splits * batches.
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kSimtThreads)
+    simt_product_kernel(Operand A, Operand Bo, int M, int N, int64_t Kk, int mt, int nt, int64_t kper, Epi p) {
+    __shared__ float sa[SK][ST + 4], sb[SK][ST + 4];
+    int64_t id = blockIdx.x;
+    const int n0 = static_cast<int>(id % nt) * ST;
+    const int tile = static_cast<int>(id % nt);
+    id /= nt;
+    const int m0 = static_cast<int>(id % mt) * ST;
+    id /= mt;
+    const int split = static_cast<int>(id % p.splits);
+    const int64_t b = id / p.splits, nb = gridDim.x / (static_cast<int64_t>(nt) * mt * p.splits);
+    const int64_t kb = split * kper, ke = min(Kk, kb + kper);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float acc[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    for (int64_t k = kb; k < ke; k += SK) {
+        simt_stage<T>(A, b, m0, M, k, ke, sa);
+        simt_stage<T>(Bo, b, n0, N, k, ke, sb);
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < SK; ++q) {
+            float av[8], bv[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                av[i] = sa[q][ty * 4 + i];
+                av[i + 4] = sa[q][64 + ty * 4 + i];
+                bv[i] = sb[q][tx * 4 + i];
+                bv[i + 4] = sb[q][64 + tx * 4 + i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        }
+        __syncthreads();
+    }
+    const float inv = MODE == kOut && p.splits == 1 ? pow2_factor(p.wmax, true) : 1.f;
+    const float fac = MODE == kProb ? pow2_factor(p.wmax, false) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = m0 + (i & 3) + ty * 4 + (i >> 2) * 64;
+        const bool rin = row < M;
+        const int64_t br = b * M + row;
+        if (MODE == kLse) {
+            float m = -INFINITY;
+            const int label = rin ? p.ids[br] : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int col = n0 + (j & 3) + tx * 4 + (j >> 2) * 64;
+                acc[i][j] *= p.scale;
+                if (col < N) {
+                    m = fmaxf(m, acc[i][j]);
+                    if (col == label) p.zt[br] = acc[i][j];
+                }
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int col = n0 + (j & 3) + tx * 4 + (j >> 2) * 64;
+                if (col < N) s += expf(acc[i][j] - m);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (tx == 0 && rin) p.pairs[(b * nt + tile) * M + row] = make_float2(m, s);
+        } else if (MODE == kProb) {
+            if (!rin) continue;
+            const int label = p.ids[br];
+            const bool has = label >= 0 && label < p.K;
+            const float w = p.w[br] * fac, lse = p.lse[br];
+            T *Pr = static_cast<T *>(p.P) + br * p.ldp;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int col = n0 + (j & 3) + tx * 4 + (j >> 2) * 64;
+                if (col < N) {
+                    const float q = expf(fmaf(p.scale, acc[i][j], -lse)) - (p.k0 + col == label ? 1.f : 0.f);
+                    Pr[col] = Cvt<T>::from_f(has ? w * q : 0.f);
+                }
+            }
+        } else {
+            if (!rin) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int col = n0 + (j & 3) + tx * 4 + (j >> 2) * 64;
+                if (col >= N) continue;
+                const int64_t at = br * N + col;
+                if (p.splits > 1) {
+                    p.out32[(split * nb * M) * N + at] = acc[i][j];
+                } else {
+                    const float v = acc[i][j] * inv + (p.acc ? p.acc[at] : 0.f);
+                    if (p.out32) p.out32[at] = v;
+                    else static_cast<T *>(p.outT)[at] = Cvt<T>::from_f(v);
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ small kernels around them
+
+// loss and lse from the per-tile pairs: 32 rows x 8 slices of the tiles per block, slices and
+// tiles joined in a fixed order.
+__global__ void __launch_bounds__(256)
+    lse_join_kernel(const float2 *__restrict__ pairs, const float *__restrict__ zt, const int32_t *__restrict__ ids,
+                    int64_t B, int N, int K, int tiles, float *__restrict__ loss, float *__restrict__ lse) {
+    __shared__ float sm[8][32], ss[8][32];
+    const int x = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const int64_t per = (N + 31) / 32;
+    const int64_t b = blockIdx.x / per;
+    const int row = static_cast<int>(blockIdx.x % per) * 32 + x;
+    const float2 *pr = pairs + b * tiles * N + row;
+    float m = -INFINITY, s = 0.f;
+    if (row < N)
+        for (int t = q; t < tiles; t += 8) {
+            const float2 v = pr[static_cast<int64_t>(t) * N];
+            const float mm = fmaxf(m, v.x);
+            s = s * expf(m - mm) + v.y * expf(v.x - mm);
+            m = mm;
+        }
+    sm[q][x] = m;
+    ss[q][x] = s;
+    __syncthreads();
+    if (q == 0 && row < N) {
+        for (int i = 1; i < 8; ++i)
+            if (i < tiles) {
+                const float mm = fmaxf(m, sm[i][x]);
+                s = s * expf(m - mm) + ss[i][x] * expf(sm[i][x] - mm);
+                m = mm;
+            }
+        const float l = m + logf(s);
+        const int64_t at = b * N + row;
+        const int id = ids[at];
+        if (lse) lse[at] = l;
+        if (loss) loss[at] = id >= 0 && id < K ? l - zt[at] : 0.f;
+    }
+}
+
+// w[b,n] = g[b,n] * scale, 0 without a label; with wmax the bits of max |w| (order of the atomics
+// does not matter to a maximum).
+__global__ void __launch_bounds__(256)
+    weight_kernel(const float *__restrict__ g, const int32_t *__restrict__ ids, int64_t rows, int K, float scale,
+                  float *__restrict__ w, unsigned int *__restrict__ wmax) {
+    const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+    float v = 0.f;
+    if (i < rows) {
+        const int id = ids[i];
+        if (id >= 0 && id < K) v = (g ? g[i] : 1.f) * scale;
+        w[i] = v;
+    }
+    if (wmax) {
+        const unsigned int m = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v)));
+        if ((threadIdx.x & 31) == 0 && m) atomicMax(wmax, m);
+    }
+}
+
+// Rows of src [rows, d] to dst [rows, dp] (dp >= d, the rest zeros); with ids, rows without a
+// label become zeros, so that whatever they hold cannot reach a sum over rows.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    copy_rows_kernel(const T *__restrict__ src, const int32_t *__restrict__ ids, int64_t rows, int d, int dp, int K,
+                     T *__restrict__ dst) {
+    const int64_t total = rows * dp;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const int64_t r = i / dp;
+        const int c = static_cast<int>(i - r * dp);
+        bool keep = c < d;
+        if (ids && keep) {
+            const int id = ids[r];
+            keep = id >= 0 && id < K;
+        }
+        dst[i] = keep ? src[r * d + c] : Cvt<T>::from_f(0.f);
+    }
+}
+
+// Joins the splits of a product in split order; adds acc, scales back, writes fp32 or T.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    split_join_kernel(const float *__restrict__ parts, int splits, int64_t count, Epi p) {
+    const float inv = pow2_factor(p.wmax, true);
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
+        float v = 0.f;
+        for (int s = 0; s < splits; ++s) v += parts[s * count + i];
+        v = v * inv + (p.acc ? p.acc[i] : 0.f);
+        if (p.out32) p.out32[i] = v;
+        else static_cast<T *>(p.outT)[i] = Cvt<T>::from_f(v);
+    }
+}
+
+}  // namespace xe
+}  // namespace km

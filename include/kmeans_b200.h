@@ -384,6 +384,82 @@ km_status km_encode1d(const void *X, km_dtype dtype, int64_t B, int64_t N, const
 km_status km_init_kmeanspp1d(const void *X, km_dtype dtype, const float *w, int64_t B, int64_t N,
                              int64_t K, const float *u, float *C, int32_t *chosen, void *stream);
 
+/*
+ * 4-bit codes. km_pack4 stores the codes[R,N] (uint8, as km_encode1d writes them; only the low
+ * four bits count) two to a byte, the even position in the low half, each row padded with zero
+ * codes to 16 bytes: packed[R, pitch] with pitch = 16 * ceil(N / 32).
+ *
+ * km_matvec4 multiplies M vectors with the weights those codes stand for:
+ *     y[m,r] = sum_n s[r, n / group] * T(C[r, code[r,n]]) * x[m,n]
+ * x[M,N] and y[M,R] in `dtype`; C[R,K] fp32 with K <= 16, its values rounded to `dtype` (T) as
+ * km_prep rounds centroids; a code of K or more stands for weight 0. scales[R, ceil(N/group)] fp32
+ * with group a multiple of 32, or scales NULL and group 0 (all ones). Sums and scales are fp32;
+ * y is rounded once. Values of x beyond N and codes in the padding take no part. Row r of y
+ * depends on row r of the weights and row m of x alone, so Inf or NaN there stay there.
+ * `packed` 16-byte aligned. Asynchronous on `stream`, no workspace. Errors: KM_ERR_INVALID_ARG;
+ * KM_ERR_UNSUPPORTED (K > 16, group not a multiple of 32); KM_ERR_CUDA.
+ */
+km_status km_pack4(const uint8_t *codes, int64_t R, int64_t N, uint8_t *packed, void *stream);
+km_status km_matvec4(const void *x, km_dtype dtype, int64_t M, const uint8_t *packed, const float *C,
+                     int64_t R, int64_t N, int64_t K, const float *scales, int64_t group, void *y,
+                     void *stream);
+
+/*
+ * Table lookup (the decoding side of the assignment): Y[b,n,:] = scale * C[b, ids[b,n], :], zero
+ * rows for ids outside [0,K). C[B,K,d] and Y[B,N,d] in `dtype`, the product rounded once. Values
+ * of rows that no id names are not read. Asynchronous on `stream`, no workspace.
+ * Errors: KM_ERR_INVALID_ARG, KM_ERR_CUDA.
+ */
+km_status km_lookup(const void *C, km_dtype dtype, const int32_t *ids, int64_t B, int64_t N,
+                    int64_t K, int64_t d, float scale, void *Y, void *stream);
+
+/*
+ * Gradient of km_lookup with respect to the table:
+ *     dC[b,k,:] = scale * sum_{n: ids[b,n] = k} dY[b,n,:]      (+ dC[b,k,:] with accumulate != 0)
+ * The tokens are sorted by id (stable) and each row's run is summed in fp32 in an order that the
+ * sizes and ids alone fix, so equal calls give equal bits. Ids outside [0,K) are ignored, their
+ * rows of dY not read. Without accumulate, rows without tokens are set to zero; with it they are
+ * left as they are. dY[B,N,d] in `dtype`; dC[B,K,d] in `out_dtype`, which is `dtype` or fp32.
+ * ws: km_lookup_grad_workspace_size(...) bytes, 256-byte aligned (0 is returned for sizes that
+ * are not provided). Asynchronous on `stream`. Errors: KM_ERR_INVALID_ARG; KM_ERR_UNSUPPORTED
+ * (B*N or B*K of 2^31 or more, other out_dtype); KM_ERR_WORKSPACE; KM_ERR_CUDA.
+ */
+size_t km_lookup_grad_workspace_size(int64_t B, int64_t N, int64_t K, int64_t d);
+km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int64_t B, int64_t N,
+                         int64_t K, int64_t d, float scale, void *dC, km_dtype out_dtype,
+                         int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Softmax cross entropy of points against all K rows of a table (the soft counterpart of
+ * km_assign, training on the ids it gives), without storing the N x K logits:
+ *     z[n,k] = scale * <X[b,n], C[b,k]>,  lse[b,n] = log sum_k exp(z[n,k]),
+ *     loss[b,n] = lse[b,n] - z[n, ids[b,n]], 0 where ids[b,n] is outside [0,K) (no label).
+ * X[B,N,d], C[B,K,d] in `dtype`; loss[B,N], lse[B,N] fp32 out, either may be NULL.
+ *
+ * km_xent_grad: with P[n,k] = g[n] * scale * (exp(z[n,k] - lse[n]) - [k = id_n]), 0 for points
+ * without a label,
+ *     dX[b,n] = sum_k P[n,k] C[b,k],      dC[b,k] = sum_n P[n,k] X[b,n].
+ * lse as km_xent wrote it; g[B,N] fp32, the gradient of each loss, NULL = all ones; dX[B,N,d],
+ * dC[B,K,d] in `dtype`, either may be NULL. The logits are computed again, one piece of the table
+ * at a time, and P is held in `dtype` (fp16: scaled by a power of two that takes the largest
+ * |g * scale| to [2^14, 2^15), so that small probabilities keep their bits); all sums are fp32,
+ * in an order fixed by the sizes. Points without a label may hold any values: they reach
+ * neither gradient (their own rows of dX are zero).
+ *
+ * ws: km_xent_workspace_size / km_xent_grad_workspace_size bytes, 256-byte aligned (0 for sizes
+ * that are not provided). Asynchronous on `stream`. Errors: KM_ERR_INVALID_ARG;
+ * KM_ERR_UNSUPPORTED (B*N, or B * ceil(N/128) * ceil(K/128), of 2^31 or more);
+ * KM_ERR_WORKSPACE; KM_ERR_CUDA.
+ */
+size_t km_xent_workspace_size(int64_t B, int64_t N, int64_t K, int64_t d, km_dtype dtype);
+km_status km_xent(const void *X, km_dtype dtype, const void *C, const int32_t *ids, int64_t B,
+                  int64_t N, int64_t K, int64_t d, float scale, float *loss, float *lse, void *ws,
+                  size_t ws_bytes, void *stream);
+size_t km_xent_grad_workspace_size(int64_t B, int64_t N, int64_t K, int64_t d, km_dtype dtype);
+km_status km_xent_grad(const void *X, km_dtype dtype, const void *C, const int32_t *ids,
+                       const float *lse, const float *g, int64_t B, int64_t N, int64_t K, int64_t d,
+                       float scale, void *dX, void *dC, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
