@@ -11,6 +11,15 @@
 
 #include "kmeans_b200.h"
 
+// The device error word and the wait limit of km_common.cuh exist once per translation unit; the
+// unit of the cross entropy exports its own for km_device_error and km_debug_wait_limit.
+namespace km {
+namespace xe {
+cudaError_t take_device_error(unsigned int *bits);            // reads and clears
+cudaError_t set_wait_limit(unsigned long long limit_ns);
+}  // namespace xe
+}  // namespace km
+
 namespace {
 
 constexpr size_t kAlign = 256;

@@ -1,8 +1,8 @@
 // km_lib.cu -- the C ABI of libkmeans_b200.so (declared in include/kmeans_b200.h).
 //
-// Argument validation, workspace carving, kernel selection and stream-ordered launches. All
-// kernels live in the km_*.cuh headers of this directory and are compiled in this single
-// translation unit. The library never allocates device memory: every scratch buffer is carved
+// Argument validation, workspace carving, kernel selection and stream-ordered launches. The
+// k-means kernels live in the km_*.cuh headers of this directory and are compiled in this
+// translation unit (the codebook operators have units of their own). The library never allocates device memory: every scratch buffer is carved
 // from the caller's workspace, whose size km_workspace_size computes with the same layout code.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -1652,6 +1652,9 @@ km_status km_device_error(void *stream, int *code) {
     if (cudaMemcpyFromSymbol(&v, km::g_km_dev_error, sizeof(v)) != cudaSuccess ||
         cudaMemcpyToSymbol(km::g_km_dev_error, &zero, sizeof(zero)) != cudaSuccess)
         return KM_ERR_CUDA;
+    unsigned int other = 0;
+    if (km::xe::take_device_error(&other) != cudaSuccess) return KM_ERR_CUDA;
+    v |= other;
     *code = static_cast<int>(v);
     return v ? KM_ERR_DEVICE_TIMEOUT : KM_OK;
 }
@@ -1661,7 +1664,8 @@ km_status km_debug_wait_limit(unsigned long long limit_ns, unsigned long long *p
     unsigned long long old = 0;
     if (cudaDeviceSynchronize() != cudaSuccess ||
         cudaMemcpyFromSymbol(&old, km::g_km_wait_limit_ns, sizeof(old)) != cudaSuccess ||
-        cudaMemcpyToSymbol(km::g_km_wait_limit_ns, &limit_ns, sizeof(limit_ns)) != cudaSuccess)
+        cudaMemcpyToSymbol(km::g_km_wait_limit_ns, &limit_ns, sizeof(limit_ns)) != cudaSuccess ||
+        km::xe::set_wait_limit(limit_ns) != cudaSuccess)
         return KM_ERR_CUDA;
     if (previous_ns) *previous_ns = old;
     return KM_OK;

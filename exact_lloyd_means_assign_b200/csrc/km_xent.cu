@@ -1,7 +1,10 @@
 // km_xent.cu -- softmax cross entropy over a table: C entry points, workspaces and launches
 // (kernels in km_xent.cuh).
+#include <type_traits>
+
 #include "km_host.h"
 #include "km_xent.cuh"
+#include "km_xent_tc.cuh"
 
 namespace {
 
@@ -15,33 +18,49 @@ inline bool xent_sizes_ok(int64_t B, int64_t N, int64_t K, int64_t d) {
            B * ceil_div(N, ST) * ceil_div(K, ST) <= kMaxIndex;
 }
 
-struct LossWs {
-    float2 *pairs;
-    float *zt;
-};
-inline LossWs carve_loss(Carver &c, int64_t B, int64_t N, int64_t K) {
-    LossWs w;
-    w.pairs = c.take<float2>(static_cast<size_t>(B * ceil_div(K, ST) * N) * 8);
-    w.zt = c.take<float>(static_cast<size_t>(B * N) * 4);
-    return w;
-}
-
 // Table rows per piece of the gradient.
 inline int64_t piece_rows(int64_t B, int64_t N, int64_t K) {
     const int64_t all = ceil_div(K, kPieceStep) * kPieceStep;
     const int64_t fit = kPieceElems / (B * N) / kPieceStep * kPieceStep;
     return std::min(all, std::max<int64_t>(kPieceStep, fit));
 }
-// Splits of a product's reduction: only where the output tiles alone leave SMs idle, each split
-// at least 512 long.
-inline int64_t product_splits(int64_t B, int64_t M, int64_t N, int64_t Kk) {
-    const int64_t tiles = B * ceil_div(M, ST) * ceil_div(N, ST);
+// Splits of a product's reduction, each a multiple of 64 long: only where the output tiles alone
+// leave SMs idle, each split at least 512 long. The tensor cores work on 256 x 256 (or 128) tiles
+// per SM pair, the CUDA cores on 128 x 128 per SM.
+inline int64_t tc_bn_out(int64_t N) { return N > 128 ? 256 : 128; }
+inline int64_t product_splits(int64_t B, int64_t M, int64_t N, int64_t Kk, km_dtype dt) {
+    const int64_t tiles = dt == KM_F32 ? B * ceil_div(M, ST) * ceil_div(N, ST)
+                                       : 2 * B * ceil_div(M, 256) * ceil_div(N, tc_bn_out(N));
     if (tiles >= 148) return 1;
-    return std::max<int64_t>(1, std::min(ceil_div(2 * 148, tiles), Kk / 512));
+    const int64_t want = std::max<int64_t>(1, std::min(ceil_div(148, tiles), Kk / 512));
+    const int64_t per = ceil_div(ceil_div(Kk, TKC), want);
+    return ceil_div(ceil_div(Kk, TKC), per);
+}
+
+// fp16 and bf16 run on the tensor cores. Rows that are no multiple of 16 bytes are copied to padded
+// ones first; rows that are, but in a buffer that does not start on 16 bytes, take the CUDA cores.
+inline int64_t padded(int64_t d, km_dtype dt) { return dt == KM_F32 ? d : ceil_div(d, 8) * 8; }
+inline bool use_tc(km_dtype dt, int64_t d, const void *X, const void *C) {
+    return dt != KM_F32 && (d % 8 != 0 || (aligned(X, 16) && aligned(C, 16))) && encode_fn() != nullptr;
+}
+
+struct LossWs {
+    float2 *pairs;
+    float *zt;
+    void *X, *C;    // padded copies, or null
+};
+inline LossWs carve_loss(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d, km_dtype dt) {
+    LossWs w;
+    const int64_t dp = padded(d, dt);
+    w.X = dp != d ? c.take<uint8_t>(static_cast<size_t>(B * N * dp) * 2) : nullptr;
+    w.C = dp != d ? c.take<uint8_t>(static_cast<size_t>(B * K * dp) * 2) : nullptr;
+    w.pairs = c.take<float2>(static_cast<size_t>(B * ceil_div(K, ST) * N) * 8);
+    w.zt = c.take<float>(static_cast<size_t>(B * N) * 4);
+    return w;
 }
 
 struct GradWs {
-    void *P, *X;
+    void *P, *X, *C;
     float *w, *parts, *dxacc;
     unsigned int *wmax;
 };
@@ -49,14 +68,16 @@ inline GradWs carve_grad(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d, 
     GradWs g;
     const int64_t kc = piece_rows(B, N, K);
     g.P = c.take<uint8_t>(static_cast<size_t>(B * N * kc) * dtype_size(dt));
-    g.X = c.take<uint8_t>(static_cast<size_t>(B * N * d) * dtype_size(dt));
+    const int64_t dp = padded(d, dt);
+    g.X = c.take<uint8_t>(static_cast<size_t>(B * N * dp) * dtype_size(dt));
+    g.C = dp != d ? c.take<uint8_t>(static_cast<size_t>(B * K * dp) * 2) : nullptr;
     g.w = c.take<float>(static_cast<size_t>(B * N) * 4);
     g.wmax = c.take<unsigned int>(4);
     int64_t parts = 0;
     for (int64_t k0 = 0; k0 < K; k0 += kc) {
         const int64_t kn = std::min(kc, K - k0);
-        const int64_t sx = product_splits(B, N, d, kn), nb = kn == K ? B : 1;
-        const int64_t sc = product_splits(nb, kn, d, N);
+        const int64_t sx = product_splits(B, N, d, kn, dt), nb = kn == K ? B : 1;
+        const int64_t sc = product_splits(nb, kn, d, N, dt);
         if (sx > 1) parts = std::max(parts, sx * B * N * d);
         if (sc > 1) parts = std::max(parts, sc * nb * kn * d);
         if (k0 == 0 && K - k0 > 2 * kc) k0 += (K - k0 - 2 * kc) / kc * kc;   // whole pieces are alike
@@ -70,7 +91,7 @@ template <typename T, int MODE>
 km_status simt_product(const Operand &A, const Operand &Bo, int64_t B, int64_t M, int64_t N, int64_t Kk, Epi p,
                        int64_t splits, cudaStream_t st) {
     const int64_t mt = ceil_div(M, ST), nt = ceil_div(N, ST);
-    const int64_t kper = ceil_div(ceil_div(Kk, splits), SK) * SK;
+    const int64_t kper = ceil_div(ceil_div(Kk, TKC), splits) * TKC;
     p.splits = static_cast<int>(splits);
     const int64_t blocks = mt * nt * splits * B;
     if (blocks > kMaxIndex) return KM_ERR_UNSUPPORTED;
@@ -79,35 +100,144 @@ km_status simt_product(const Operand &A, const Operand &Bo, int64_t B, int64_t M
     return launch_status();
 }
 
+// Tensor map of an operand: K-major boxes of 64 reduction steps x `rows`, MN-major boxes of 64 rows
+// x 64 reduction steps. Every box starts on a multiple of 64 elements of its contiguous index.
+inline bool encode_operand(CUtensorMap *tm, CUtensorMapDataType tdt, const Operand &o, int64_t rows_total, int64_t Kk,
+                           int64_t B, int rows) {
+    const bool mn = o.k_s != 1;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(mn ? rows_total : Kk),
+                                static_cast<cuuint64_t>(mn ? Kk : rows_total), static_cast<cuuint64_t>(B)};
+    const int64_t ld = mn ? o.k_s : o.row_s;
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(o.batch * 2)};
+    const cuuint32_t box[3] = {TKC, static_cast<cuuint32_t>(mn ? TKC : rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_fn()(tm, tdt, 3, const_cast<void *>(o.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int BN, int MODE, bool AMN, bool BMN>
+km_status tc_launch(const Operand &A, const Operand &Bo, int64_t B, int64_t M, int64_t N, int64_t Kk, Epi e,
+                    int64_t splits, cudaStream_t st) {
+    using Sh = TcShape<BN>;
+    const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    const CUtensorMapDataType tdt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap tmA, tmB;
+    if (!encode_operand(&tmA, tdt, A, M, Kk, B, TBM) || !encode_operand(&tmB, tdt, Bo, N, Kk, B, BN / 2))
+        return KM_ERR_CUDA;
+    auto kernel = tc_product_kernel<T, BN, MODE, AMN, BMN>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Sh::kTotal)) !=
+        cudaSuccess)
+        return KM_ERR_CUDA;
+    // persistent SM pairs: as many as can be resident (a pair needs two SMs of one GPC)
+    static int resident[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int clusters = (dev >= 0 && dev < 64) ? resident[dev] : 0;
+    if (clusters <= 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * std::max(1, num_sms() / 2)));
+        cfg.blockDim = dim3(T_THREADS);
+        cfg.dynamicSmemBytes = Sh::kTotal;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters <= 0) {
+            cudaGetLastError();
+            clusters = std::max(1, num_sms() / 2);
+        }
+        if (dev >= 0 && dev < 64) resident[dev] = clusters;
+    }
+    TcParams p = {};
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.mt = static_cast<int>(ceil_div(M, 2 * TBM));
+    p.nt = static_cast<int>(ceil_div(N, BN));
+    p.nb = static_cast<int>(B);
+    p.Kk = static_cast<int>(Kk);
+    p.kchunks = static_cast<int>(ceil_div(Kk, TKC));
+    p.kper = static_cast<int>(ceil_div(p.kchunks, splits));
+    p.idesc = km::mma_idesc_f16(bf16 ? 1u : 0u, 2 * TBM, BN) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+    p.vec = N % 8 == 0 && (!e.outT || aligned(e.outT, 16)) ? 1 : 0;
+    e.splits = static_cast<int>(splits);
+    const int64_t items = static_cast<int64_t>(p.mt) * p.nt * splits * B;
+    if (items > kMaxIndex) return KM_ERR_UNSUPPORTED;
+    const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(items, clusters));
+    kernel<<<grid, T_THREADS, Sh::kTotal, st>>>(tmA, tmB, p, e);
+    return launch_status();
+}
+
+template <typename T, int MODE>
+km_status product(bool tc, const Operand &A, const Operand &Bo, int64_t B, int64_t M, int64_t N, int64_t Kk,
+                  const Epi &p, int64_t splits, cudaStream_t st) {
+    if constexpr (!std::is_same<T, float>::value) {
+        if (tc) {
+            if constexpr (MODE != kOut) {
+                return tc_launch<T, 256, MODE, false, false>(A, Bo, B, M, N, Kk, p, splits, st);
+            } else {
+                const bool wide = tc_bn_out(N) == 256;
+                if (A.k_s == 1)     // dX = P C
+                    return wide ? tc_launch<T, 256, kOut, false, true>(A, Bo, B, M, N, Kk, p, splits, st)
+                                : tc_launch<T, 128, kOut, false, true>(A, Bo, B, M, N, Kk, p, splits, st);
+                return wide ? tc_launch<T, 256, kOut, true, true>(A, Bo, B, M, N, Kk, p, splits, st)
+                            : tc_launch<T, 128, kOut, true, true>(A, Bo, B, M, N, Kk, p, splits, st);
+            }
+        }
+    }
+    return simt_product<T, MODE>(A, Bo, B, M, N, Kk, p, splits, st);
+}
+
 inline unsigned fill_blocks(int64_t n) {
     return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ceil_div(n, 256), 148 * 16)));
 }
 
 // out = A B (+ acc), through split partials where the reduction is split.
 template <typename T>
-km_status out_product(const Operand &A, const Operand &Bo, int64_t B, int64_t M, int64_t N, int64_t Kk, Epi p,
-                      float *parts, cudaStream_t st) {
-    const int64_t splits = product_splits(B, M, N, Kk);
-    if (splits == 1) return simt_product<T, kOut>(A, Bo, B, M, N, Kk, p, 1, st);
+km_status out_product(bool tc, km_dtype dt, const Operand &A, const Operand &Bo, int64_t B, int64_t M, int64_t N,
+                      int64_t Kk, Epi p, float *parts, cudaStream_t st) {
+    const int64_t splits = product_splits(B, M, N, Kk, dt);
+    if (splits == 1) return product<T, kOut>(tc, A, Bo, B, M, N, Kk, p, 1, st);
     Epi q = p;
     q.out32 = parts;
-    km_status s = simt_product<T, kOut>(A, Bo, B, M, N, Kk, q, splits, st);
+    q.outT = nullptr;
+    km_status s = product<T, kOut>(tc, A, Bo, B, M, N, Kk, q, splits, st);
     if (s != KM_OK) return s;
     split_join_kernel<T><<<fill_blocks(B * M * N), 256, 0, st>>>(parts, static_cast<int>(splits), B * M * N, p);
     return launch_status();
 }
 
 template <typename T>
-km_status loss_typed(const void *X, const void *C, const int32_t *ids, int64_t B, int64_t N, int64_t K, int64_t d,
-                     float scale, float *loss, float *lse, const LossWs &w, cudaStream_t st) {
+km_status copy_rows(const void *src, const int32_t *ids, int64_t rows, int64_t d, int64_t dp, int64_t K, void *dst,
+                    cudaStream_t st) {
+    copy_rows_kernel<T><<<fill_blocks(rows * dp), 256, 0, st>>>(static_cast<const T *>(src), ids, rows,
+                                                                static_cast<int>(d), static_cast<int>(dp),
+                                                                static_cast<int>(K), static_cast<T *>(dst));
+    return launch_status();
+}
+
+template <typename T>
+km_status loss_typed(const void *X, km_dtype dt, const void *C, const int32_t *ids, int64_t B, int64_t N, int64_t K,
+                     int64_t d, float scale, float *loss, float *lse, const LossWs &w, cudaStream_t st) {
+    const bool tc = use_tc(dt, d, X, C);
+    const int64_t dp = tc ? padded(d, dt) : d;
+    km_status s;
+    if (dp != d) {
+        if ((s = copy_rows<T>(X, nullptr, B * N, d, dp, K, w.X, st)) != KM_OK) return s;
+        if ((s = copy_rows<T>(C, nullptr, B * K, d, dp, K, w.C, st)) != KM_OK) return s;
+        X = w.X;
+        C = w.C;
+    }
     Epi p = {};
     p.scale = scale;
     p.pairs = w.pairs;
     p.zt = w.zt;
     p.ids = ids;
     p.K = static_cast<int>(K);
-    const Operand A = {X, N * d, d, 1}, Bo = {C, K * d, d, 1};
-    km_status s = simt_product<T, kLse>(A, Bo, B, N, K, d, p, 1, st);
+    s = product<T, kLse>(tc, Operand{X, N * dp, dp, 1}, Operand{C, K * dp, dp, 1}, B, N, K, dp, p, 1, st);
     if (s != KM_OK) return s;
     lse_join_kernel<<<static_cast<unsigned>(B * ceil_div(N, 32)), 256, 0, st>>>(
         w.pairs, w.zt, ids, B, static_cast<int>(N), static_cast<int>(K), static_cast<int>(ceil_div(K, ST)), loss, lse);
@@ -120,21 +250,27 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
                      cudaStream_t st) {
     Carver cv(ws);
     const GradWs w = carve_grad(cv, B, N, K, d, dt);
+    const bool tc = use_tc(dt, d, X, C);
+    const int64_t dp = tc ? padded(d, dt) : d;
+    km_status s;
     unsigned int *wmax = dt == KM_F16 ? w.wmax : nullptr;
     if (wmax && cudaMemsetAsync(wmax, 0, 4, st) != cudaSuccess) return KM_ERR_CUDA;
     km::xe::weight_kernel<<<static_cast<unsigned>(ceil_div(B * N, 256)), 256, 0, st>>>(
         g, ids, B * N, static_cast<int>(K), scale, w.w, wmax);
     if (launch_status() != KM_OK) return KM_ERR_CUDA;
-    if (dC) {
-        copy_rows_kernel<T><<<fill_blocks(B * N * d), 256, 0, st>>>(
-            static_cast<const T *>(X), ids, B * N, static_cast<int>(d), static_cast<int>(d), static_cast<int>(K),
-            static_cast<T *>(w.X));
-        if (launch_status() != KM_OK) return KM_ERR_CUDA;
+    if (dC || dp != d) {
+        // points without a label become zeros here, so that nothing they hold reaches dC
+        if ((s = copy_rows<T>(X, ids, B * N, d, dp, K, w.X, st)) != KM_OK) return s;
+        X = w.X;
+    }
+    if (dp != d) {
+        if ((s = copy_rows<T>(C, nullptr, B * K, d, dp, K, w.C, st)) != KM_OK) return s;
+        C = w.C;
     }
     const int64_t kc = piece_rows(B, N, K);
     for (int64_t k0 = 0; k0 < K; k0 += kc) {
         const int64_t kn = std::min(kc, K - k0);
-        const T *Ck = static_cast<const T *>(C) + k0 * d;
+        const T *Ck = static_cast<const T *>(C) + k0 * dp;
         Epi p = {};
         p.scale = scale;
         p.ids = ids;
@@ -145,7 +281,7 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
         p.P = w.P;
         p.ldp = kc;
         p.wmax = wmax;
-        km_status s = simt_product<T, kProb>(Operand{X, N * d, d, 1}, Operand{Ck, K * d, d, 1}, B, N, kn, d, p, 1, st);
+        s = product<T, kProb>(tc, Operand{X, N * dp, dp, 1}, Operand{Ck, K * dp, dp, 1}, B, N, kn, dp, p, 1, st);
         if (s != KM_OK) return s;
         if (dX) {
             Epi q = {};
@@ -153,7 +289,8 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
             q.acc = k0 ? w.dxacc : nullptr;
             if (k0 + kc < K) q.out32 = w.dxacc;
             else q.outT = dX;
-            s = out_product<T>(Operand{w.P, N * kc, kc, 1}, Operand{Ck, K * d, 1, d}, B, N, d, kn, q, w.parts, st);
+            s = out_product<T>(tc, dt, Operand{w.P, N * kc, kc, 1}, Operand{Ck, K * dp, 1, dp}, B, N, d, kn, q, w.parts,
+                               st);
             if (s != KM_OK) return s;
         }
         if (dC) {
@@ -164,8 +301,8 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
             const int64_t nb = kn == K ? B : 1;
             for (int64_t b = 0; b < B; b += nb) {
                 q.outT = static_cast<T *>(dC) + (b * K + k0) * d;
-                s = out_product<T>(Operand{static_cast<const T *>(w.P) + b * N * kc, N * kc, 1, kc},
-                                   Operand{static_cast<const T *>(w.X) + b * N * d, N * d, 1, d}, nb, kn, d, N, q,
+                s = out_product<T>(tc, dt, Operand{static_cast<const T *>(w.P) + b * N * kc, N * kc, 1, kc},
+                                   Operand{static_cast<const T *>(X) + b * N * dp, N * dp, 1, dp}, nb, kn, d, N, q,
                                    w.parts, st);
                 if (s != KM_OK) return s;
             }
@@ -176,12 +313,27 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
 
 }  // namespace
 
+namespace km {
+namespace xe {
+
+cudaError_t take_device_error(unsigned int *bits) {
+    const unsigned int zero = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_km_dev_error, sizeof(*bits));
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_km_dev_error, &zero, sizeof(zero));
+}
+cudaError_t set_wait_limit(unsigned long long limit_ns) {
+    return cudaMemcpyToSymbol(g_km_wait_limit_ns, &limit_ns, sizeof(limit_ns));
+}
+
+}  // namespace xe
+}  // namespace km
+
 extern "C" {
 
 size_t km_xent_workspace_size(int64_t B, int64_t N, int64_t K, int64_t d, km_dtype dtype) {
     if (!valid_dtype(dtype) || !xent_sizes_ok(B, N, K, d)) return 0;
     Carver c(nullptr);
-    carve_loss(c, B, N, K);
+    carve_loss(c, B, N, K, d, dtype);
     return c.off;
 }
 
@@ -194,11 +346,11 @@ km_status km_xent(const void *X, km_dtype dtype, const void *C, const int32_t *i
     if (!xent_sizes_ok(B, N, K, d)) return KM_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < km_xent_workspace_size(B, N, K, d, dtype)) return KM_ERR_WORKSPACE;
     Carver c(ws);
-    const LossWs w = carve_loss(c, B, N, K);
+    const LossWs w = carve_loss(c, B, N, K, d, dtype);
     switch (dtype) {
-        case KM_F32: return loss_typed<float>(X, C, ids, B, N, K, d, scale, loss, lse, w, S(stream));
-        case KM_F16: return loss_typed<__half>(X, C, ids, B, N, K, d, scale, loss, lse, w, S(stream));
-        default: return loss_typed<__nv_bfloat16>(X, C, ids, B, N, K, d, scale, loss, lse, w, S(stream));
+        case KM_F32: return loss_typed<float>(X, dtype, C, ids, B, N, K, d, scale, loss, lse, w, S(stream));
+        case KM_F16: return loss_typed<__half>(X, dtype, C, ids, B, N, K, d, scale, loss, lse, w, S(stream));
+        default: return loss_typed<__nv_bfloat16>(X, dtype, C, ids, B, N, K, d, scale, loss, lse, w, S(stream));
     }
 }
 

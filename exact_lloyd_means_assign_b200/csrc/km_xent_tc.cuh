@@ -1,0 +1,401 @@
+// km_xent_tc.cuh -- the products of the cross entropy and its gradients on the 5th-generation
+// tensor cores (tcgen05, TMEM, TMA), one SM pair per 256 x BN tile (cta_group::2).
+//
+// One kernel forms D[m,n] = sum_k A(m,k) B(n,k) for the three products and differs in how the
+// operands lie in memory and in what becomes of a tile:
+//   kLse   A = X, B = C, reduction over d: the tile's logits become one (maximum, sum of
+//          exponentials) pair per row and 128 columns
+//   kProb  the same logits become P, in the points' type
+//   kOut   dX = P C (reduction over the table piece) and dC = P^T X (reduction over the points)
+// An operand whose reduction index is the contiguous one is staged K-major, the others MN-major,
+// so P, X and C are read as they lie and nothing is transposed in memory.
+//
+// Shared memory per CTA and stage of 64 reduction steps: 128 rows of A (16 KB) and BN / 2 of B;
+// both CTAs of a pair stage half of B, which the pair's MMAs share. The 512 TMEM columns hold two
+// accumulators, so a tile's epilogue runs while the next tile is computed.
+//
+// Roles per CTA (12 warps): warp 0 requests the tiles; warp 1 of the leader issues the MMAs;
+// warps 4-11 are the epilogue (TMEM lane quarter = warp % 4, column half = (warp - 4) / 4, one row
+// per thread). Waits are bounded like everywhere in the library: a role that gives up sets the
+// CTA's abort flag, the producer waits for the copies it asked for, the issuer for its MMAs, the
+// pair synchronises and frees TMEM. No TMA load uses multicast.
+#pragma once
+
+#include "km_assign_tc.cuh"
+#include "km_xent.cuh"
+
+namespace km {
+namespace xe {
+
+constexpr int TBM = 128;                 // rows per CTA, 256 per pair
+constexpr int TKC = 64;                  // reduction steps per stage (128 bytes of 16-bit values)
+constexpr int T_EPI0 = 4, T_EPI_WARPS = 8;
+constexpr int T_THREADS = 32 * (T_EPI0 + T_EPI_WARPS);
+constexpr int T_GROUP = 8;               // row tiles that share their column tiles in L2
+
+template <int BN> struct TcShape {
+    static constexpr uint32_t kA = TBM * 128u, kB = (BN / 2) * 128u;
+    static constexpr uint32_t kStage = kA + kB;
+    static constexpr int kStages = BN == 256 ? 6 : 8;
+    static constexpr uint32_t kBarOff = kStages * kStage;
+    static constexpr int kBars = 2 * kStages + 5;
+    static constexpr uint32_t kTotal = kBarOff + kBars * 8 + 16 + 1024;
+};
+
+struct TcParams {
+    int M, N;             // rows and columns of D
+    int mt, nt;           // pair tiles
+    int nb;               // batches
+    int kchunks, kper;    // 64-wide chunks of the reduction, and per split
+    int Kk;
+    uint32_t idesc;
+    int vec;              // rows of the output start on 16-byte boundaries
+};
+
+struct TcItem {
+    int m, n, split, b;
+};
+__device__ __forceinline__ TcItem tc_item(const TcParams &p, int splits, int t) {
+    TcItem it;
+    const int tiles = p.mt * p.nt, per = tiles * splits;
+    it.b = t / per;
+    int r = t - it.b * per;
+    it.split = r / tiles;
+    r -= it.split * tiles;
+    const int g = r / (T_GROUP * p.nt);
+    r -= g * T_GROUP * p.nt;
+    const int size = min(T_GROUP, p.mt - g * T_GROUP);
+    it.n = r / size;
+    it.m = g * T_GROUP + (r - it.n * size);
+    return it;
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Descriptor words of an operand. K-major: 128-byte rows, the 8-row groups 1024 bytes apart, 16
+// reduction steps = 32 bytes further. MN-major: blocks of 64 rows (128 bytes) x 64 reduction steps,
+// the blocks 8192 bytes apart (leading offset), groups of 8 steps 1024 bytes apart, 16 reduction
+// steps = 2048 bytes further.
+template <bool MN> __device__ __forceinline__ uint32_t op_desc_lo(uint32_t saddr) {
+    return ((MN ? 8192u >> 4 : 1u) << 16) | (saddr >> 4);
+}
+template <bool MN> __device__ __forceinline__ constexpr uint32_t op_step() { return MN ? 2048u >> 4 : 2u; }
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <typename T, int BN, int MODE, bool AMN, bool BMN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
+    tc_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const TcParams p, const Epi ep) {
+    using Sh = TcShape<BN>;
+    using namespace km::tc;
+    constexpr int S = Sh::kStages;
+    constexpr int HALF = BN / 2;             // columns per epilogue warp
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int abort_flag;
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t *sgen = smem_raw + (sbase - raw);
+    const uint32_t bar0 = sbase + Sh::kBarOff;
+    auto FULL = [&](int s) { return bar0 + 8u * s; };
+    auto EMPTY = [&](int s) { return bar0 + 8u * (S + s); };
+    auto ACC_FULL = [&](int i) { return bar0 + 8u * (2 * S + i); };
+    auto ACC_EMPTY = [&](int i) { return bar0 + 8u * (2 * S + 2 + i); };
+    const uint32_t DRAIN = bar0 + 8u * (2 * S + 4);
+    const uint32_t slot = bar0 + 8u * Sh::kBars;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    volatile int *abortp = &abort_flag;
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < S; ++s) {
+            mbar_init(FULL(s), 1);
+            mbar_init(EMPTY(s), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(ACC_FULL(i), 1);
+            mbar_init(ACC_EMPTY(i), 2 * T_EPI_WARPS);   // (leader) the epilogue warps of both CTAs
+        }
+        mbar_init(DRAIN, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(slot, TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(sgen + (slot - sbase));
+    const int total = p.mt * p.nt * ep.splits * p.nb;
+    const int t0 = blockIdx.x >> 1, tstep = gridDim.x >> 1;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        const uint64_t pol = l2_policy_evict_last();
+        int stage = 0;
+        uint32_t ph = 0;
+        long long uses = 0;
+        bool ok = true;
+        for (int t = t0; t < total && ok; t += tstep) {
+            const TcItem it = tc_item(p, ep.splits, t);
+            const int mrow = it.m * (2 * TBM) + static_cast<int>(rank) * TBM;
+            const int nrow = it.n * BN + static_cast<int>(rank) * (BN / 2);
+            const int kc1 = min(p.kchunks, (it.split + 1) * p.kper);
+            for (int kc = it.split * p.kper; kc < kc1; ++kc) {
+                if (!mbar_wait_warp(EMPTY(stage), ph ^ 1u, abortp)) { ok = false; break; }
+                if (lane == 0) {
+                    if (leader) mbar_arrive_expect_tx(FULL(stage), 2 * Sh::kStage);
+                    const uint32_t a = sbase + stage * Sh::kStage, bsm = a + Sh::kA;
+                    const uint32_t bar = map_to_rank(FULL(stage), 0);
+                    if (AMN) {
+#pragma unroll
+                        for (int i = 0; i < TBM / 64; ++i)
+                            tma_load_3d_pair(a + i * 8192, &tmA, bar, mrow + i * 64, kc * TKC, it.b, pol);
+                    } else {
+                        tma_load_3d_pair(a, &tmA, bar, kc * TKC, mrow, it.b, pol);
+                    }
+                    if (BMN) {
+#pragma unroll
+                        for (int i = 0; i < BN / 128; ++i)
+                            tma_load_3d_pair(bsm + i * 8192, &tmB, bar, nrow + i * 64, kc * TKC, it.b, pol);
+                    } else {
+                        tma_load_3d_pair(bsm, &tmB, bar, kc * TKC, nrow, it.b, pol);
+                    }
+                }
+                __syncwarp();
+                ++uses;
+                if (++stage == S) { stage = 0; ph ^= 1u; }
+            }
+        }
+        if (!ok && leader && lane == 0) {
+            // the copies asked for land before shared memory goes away
+            for (int s = 0; s < S; ++s) {
+                const long long n = uses > s ? (uses - 1 - s) / S + 1 : 0;
+                if (n) mbar_wait(FULL(s), static_cast<uint32_t>((n - 1) & 1), nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (leader) {
+            const bool issuer = elect_one();
+            int stage = 0, buf = 0;
+            uint32_t ph = 0, aph = 0;
+            bool ok = true;
+            for (int t = t0; t < total && ok; t += tstep) {
+                const TcItem it = tc_item(p, ep.splits, t);
+                const int kc0 = it.split * p.kper, kc1 = min(p.kchunks, kc0 + p.kper);
+                if (!mbar_wait_warp(ACC_EMPTY(buf), aph ^ 1u, abortp)) break;
+                tc_fence_after();
+                const uint32_t dcol = tmem_base + buf * ACC_STRIDE;
+                for (int kc = kc0; kc < kc1; ++kc) {
+                    if (!mbar_wait_warp(FULL(stage), ph, abortp)) { ok = false; break; }
+                    tc_fence_after();
+                    if (issuer) {
+                        const uint32_t a_lo = op_desc_lo<AMN>(sbase + stage * Sh::kStage);
+                        const uint32_t b_lo = op_desc_lo<BMN>(sbase + stage * Sh::kStage + Sh::kA);
+                        const int nk = min(4, (p.Kk - kc * TKC + 15) / 16);
+                        for (int kk = 0; kk < nk; ++kk)
+                            tc_mma_pair(dcol, a_lo + kk * op_step<AMN>(), DESC_HI_SW128, b_lo + kk * op_step<BMN>(),
+                                        DESC_HI_SW128, p.idesc, (kc > kc0 || kk) ? 1u : 0u);
+                        tc_commit_pair_both(EMPTY(stage));
+                        if (kc + 1 == kc1) tc_commit_pair_both(ACC_FULL(buf));
+                    }
+                    __syncwarp();
+                    if (++stage == S) { stage = 0; ph ^= 1u; }
+                }
+                buf ^= 1;
+                if (buf == 0) aph ^= 1u;
+            }
+            // every MMA issued above completes before TMEM is released
+            if (issuer) tc_commit_pair_self(DRAIN);
+            __syncwarp();
+            mbar_wait_warp(DRAIN, 0, nullptr);
+        }
+        __syncwarp();
+    } else if (warp >= T_EPI0) {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3, half = (warp - T_EPI0) >> 2;
+        const uint32_t empty0 = map_to_rank(ACC_EMPTY(0), 0), empty1 = map_to_rank(ACC_EMPTY(1), 0);
+        const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * HALF;
+        const float s2 = ep.scale * kLog2e;
+        const float fac = MODE == kProb ? pow2_factor(ep.wmax, false) : 1.f;
+        const float inv = MODE == kOut && ep.splits == 1 ? pow2_factor(ep.wmax, true) : 1.f;
+        int buf = 0;
+        uint32_t aph = 0;
+        for (int t = t0; t < total; t += tstep) {
+            const TcItem it = tc_item(p, ep.splits, t);
+            const int row = it.m * (2 * TBM) + static_cast<int>(rank) * TBM + q * 32 + lane;
+            const int c0 = it.n * BN + half * HALF;
+            const bool rin = row < p.M;
+            const int64_t br = static_cast<int64_t>(it.b) * p.M + row;
+            int label = -1;
+            float w = 0.f, lse2 = 0.f;
+            bool has = false;
+            if (MODE != kOut && rin) {
+                label = ep.ids[br];
+                has = label >= 0 && label < ep.K;
+                label = has ? label - ep.k0 : -1;
+                if (MODE == kProb) {
+                    w = ep.w[br] * fac;
+                    lse2 = ep.lse[br] * kLog2e;
+                }
+            }
+            if (!mbar_wait_warp(ACC_FULL(buf), aph, abortp)) break;
+            tc_fence_after();
+            float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < HALF; c += 32) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tl + buf * ACC_STRIDE + c, v);
+                tmem_wait_ld(v);
+                if (c + 32 == HALF) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(buf ? empty1 : empty0);
+                }
+                const int col = c0 + c;
+                if (MODE == kLse) {
+                    if (col >= p.N) continue;
+                    float z[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        z[i] = __uint_as_float(v[i]) * s2;
+                        if (col + i >= p.N) z[i] = -INFINITY;
+                    }
+                    float cm = z[0];
+#pragma unroll
+                    for (int i = 1; i < 32; ++i) cm = fmaxf(cm, z[i]);
+                    const float nm = fmaxf(m, cm);
+                    s *= ex2f(m - nm);
+                    m = nm;
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s4[i & 3] += ex2f(z[i] - m);
+                    s += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    if (label >= col && label < col + 32) {
+                        float zt = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (col + i == label) zt = __uint_as_float(v[i]) * ep.scale;
+                        ep.zt[br] = zt;
+                    }
+                } else if (MODE == kProb) {
+                    float q32[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) q32[i] = w * ex2f(fmaf(__uint_as_float(v[i]), s2, -lse2));
+                    if (label >= col && label < col + 32) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (col + i == label) q32[i] = w * (ex2f(fmaf(__uint_as_float(v[i]), s2, -lse2)) - 1.f);
+                    }
+                    if (rin) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(ep.P) + br * ep.ldp + col);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint4 o;
+                            o.x = has ? pack2<T>(q32[i * 8], q32[i * 8 + 1]) : 0u;
+                            o.y = has ? pack2<T>(q32[i * 8 + 2], q32[i * 8 + 3]) : 0u;
+                            o.z = has ? pack2<T>(q32[i * 8 + 4], q32[i * 8 + 5]) : 0u;
+                            o.w = has ? pack2<T>(q32[i * 8 + 6], q32[i * 8 + 7]) : 0u;
+                            dst[i] = o;
+                        }
+                    }
+                } else {
+                    if (!rin || col >= p.N) continue;
+                    const int64_t at = br * p.N + col;
+                    if (ep.splits > 1) {
+                        float *dst = ep.out32 + static_cast<int64_t>(it.split) * p.nb * p.M * p.N + at;
+                        if (p.vec && col + 32 <= p.N) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                reinterpret_cast<uint4 *>(dst)[i] = make_uint4(v[i * 4], v[i * 4 + 1], v[i * 4 + 2], v[i * 4 + 3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (col + i < p.N) dst[i] = __uint_as_float(v[i]);
+                        }
+                    } else {
+                        float f[32];
+                        const bool whole = p.vec && col + 32 <= p.N;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * inv;
+                        if (ep.acc) {
+                            if (whole) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float4 a = reinterpret_cast<const float4 *>(ep.acc + at)[i];
+                                    f[i * 4] += a.x;
+                                    f[i * 4 + 1] += a.y;
+                                    f[i * 4 + 2] += a.z;
+                                    f[i * 4 + 3] += a.w;
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (col + i < p.N) f[i] += ep.acc[at + i];
+                            }
+                        }
+                        if (ep.out32) {
+                            if (whole) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    reinterpret_cast<float4 *>(ep.out32 + at)[i] =
+                                        make_float4(f[i * 4], f[i * 4 + 1], f[i * 4 + 2], f[i * 4 + 3]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (col + i < p.N) ep.out32[at + i] = f[i];
+                            }
+                        } else {
+                            T *dst = static_cast<T *>(ep.outT) + at;
+                            if (whole) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    reinterpret_cast<uint4 *>(dst)[i] =
+                                        make_uint4(pack2<T>(f[i * 8], f[i * 8 + 1]), pack2<T>(f[i * 8 + 2], f[i * 8 + 3]),
+                                                   pack2<T>(f[i * 8 + 4], f[i * 8 + 5]), pack2<T>(f[i * 8 + 6], f[i * 8 + 7]));
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (col + i < p.N) dst[i] = Cvt<T>::from_f(f[i]);
+                            }
+                        }
+                    }
+                }
+            }
+            if (MODE == kLse && rin && c0 < p.N) {
+                // pairs are kept in natural units
+                const int64_t tiles = (p.N + ST - 1) / ST;
+                ep.pairs[(static_cast<int64_t>(it.b) * tiles + it.n * 2 + half) * p.M + row] = make_float2(m / kLog2e, s);
+            }
+            buf ^= 1;
+            if (buf == 0) aph ^= 1u;
+        }
+    }
+    // both CTAs are done with each other's barriers and the leader's MMAs have drained
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+}  // namespace xe
+}  // namespace km
