@@ -129,7 +129,7 @@ def _need(t, name, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
@@ -413,38 +413,54 @@ def _dims(t, name, n):
 
 def _on_gpu(t, name):
     """The CUDA device that an operator's first argument lies on; all others must share it."""
-    if t.device.type != "cuda":
+    dev = t.device
+    if dev.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
-    _need(t, name)
-    return t.device
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return dev
 
 
 class _launch_on:
     """Makes `dev` the current device and `stream` (a torch stream, a raw cudaStream_t or None for
     the device's current stream) the current stream, so that outputs and workspaces allocated
-    inside belong to the stream that the kernels run on."""
+    inside belong to the stream that the kernels run on. The usual call, on the current stream of
+    the current device, changes nothing and enters no context."""
+
+    __slots__ = ("_raw", "_ctx")
 
     def __init__(self, dev, stream):
+        self._ctx = ()
         if stream is None:
-            self._s = torch.cuda.current_stream(dev)
-        elif hasattr(stream, "cuda_stream"):
-            self._s = stream
+            s = torch.cuda.current_stream(dev)
+            self._raw = s.cuda_stream
+            if dev.index != torch.cuda.current_device():
+                self._ctx = (torch.cuda.device(dev),)
+            return
+        if hasattr(stream, "cuda_stream"):
+            s = stream
         elif int(stream) == 0:
-            self._s = torch.cuda.default_stream(dev)
+            s = torch.cuda.default_stream(dev)
         else:
-            self._s = torch.cuda.ExternalStream(int(stream), device=dev)
-        if self._s.device != dev:
-            raise ValueError(f"the stream belongs to {self._s.device}, the tensors to {dev}")
-        self._dev, self._ctx = torch.cuda.device(dev), torch.cuda.stream(self._s)
+            s = torch.cuda.ExternalStream(int(stream), device=dev)
+        if s.device != dev:
+            raise ValueError(f"the stream belongs to {s.device}, the tensors to {dev}")
+        self._raw = s.cuda_stream
+        self._ctx = (torch.cuda.device(dev), torch.cuda.stream(s))
 
     def __enter__(self):
-        self._dev.__enter__()
-        self._ctx.__enter__()
-        return ctypes.c_void_p(self._s.cuda_stream)
+        for c in self._ctx:
+            c.__enter__()
+        return self._raw
 
     def __exit__(self, *exc):
-        self._ctx.__exit__(*exc)
-        self._dev.__exit__(*exc)
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+def _a(t):
+    """A tensor's address as ctypes takes it for a void pointer (None: null)."""
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(ws, nbytes, dev):
@@ -465,7 +481,7 @@ def km_pack4(codes, packed=None, stream=None):
         shape = (R, 16 * (-(-N // 32)))
         packed = torch.empty(shape, dtype=torch.uint8, device=dev) if packed is None else packed
         _need(packed, "packed", torch.uint8, shape, dev)
-        _check("km_pack4", _load().km_pack4(_p(codes), R, N, _p(packed), s))
+        _check("km_pack4", _load().km_pack4(_a(codes), R, N, _a(packed), s))
     return packed
 
 
@@ -491,7 +507,7 @@ def km_matvec4(x, packed, C, scales=None, group=0, y=None, stream=None):
         y = torch.empty((M, R), dtype=x.dtype, device=dev) if y is None else y
         _need(y, "y", x.dtype, (M, R), dev)
         _check("km_matvec4", _load().km_matvec4(
-            _p(x), _dt(x.dtype), M, _p(packed), _p(C), R, N, K, _p(scales), group, _p(y), s))
+            _a(x), _dt(x.dtype), M, _a(packed), _a(C), R, N, K, _a(scales), group, _a(y), s))
     return y
 
 
@@ -508,7 +524,7 @@ def km_lookup(C, ids, scale=1.0, Y=None, stream=None):
         Y = torch.empty((B, N, d), dtype=C.dtype, device=dev) if Y is None else Y
         _need(Y, "Y", C.dtype, (B, N, d), dev)
         _check("km_lookup", _load().km_lookup(
-            _p(C), _dt(C.dtype), _p(ids), B, N, K, d, float(scale), _p(Y), s))
+            _a(C), _dt(C.dtype), _a(ids), B, N, K, d, float(scale), _a(Y), s))
     return Y
 
 
@@ -530,8 +546,8 @@ def km_lookup_grad(dY, ids, K, scale=1.0, dC=None, out_dtype=None, accumulate=Fa
         _need(dC, "dC", out_dtype, (B, K, d), dev)
         ws = _scratch(ws, _load().km_lookup_grad_workspace_size(B, N, K, d), dev)
         _check("km_lookup_grad", _load().km_lookup_grad(
-            _p(dY), _dt(dY.dtype), _p(ids), B, N, K, d, float(scale), _p(dC), _dt(out_dtype),
-            int(bool(accumulate)), _p(ws), ws.numel(), s))
+            _a(dY), _dt(dY.dtype), _a(ids), B, N, K, d, float(scale), _a(dC), _dt(out_dtype),
+            int(bool(accumulate)), _a(ws), ws.numel(), s))
     return dC
 
 
@@ -553,8 +569,8 @@ def km_xent(X, C, ids, scale=1.0, loss=None, lse=None, ws=None, stream=None):
         _need(lse, "lse", torch.float32, (B, N), dev)
         ws = _scratch(ws, _load().km_xent_workspace_size(B, N, K, d, _dt(X.dtype)), dev)
         _check("km_xent", _load().km_xent(
-            _p(X), _dt(X.dtype), _p(C), _p(ids), B, N, K, d, float(scale), _p(loss), _p(lse),
-            _p(ws), ws.numel(), s))
+            _a(X), _dt(X.dtype), _a(C), _a(ids), B, N, K, d, float(scale), _a(loss), _a(lse),
+            _a(ws), ws.numel(), s))
     return loss, lse
 
 
@@ -580,8 +596,8 @@ def km_xent_grad(X, C, ids, lse, g=None, scale=1.0, dX=None, dC=None, want_dX=Tr
         _need(dC, "dC", X.dtype, (B, K, d), dev)
         ws = _scratch(ws, _load().km_xent_grad_workspace_size(B, N, K, d, _dt(X.dtype)), dev)
         _check("km_xent_grad", _load().km_xent_grad(
-            _p(X), _dt(X.dtype), _p(C), _p(ids), _p(lse), _p(g), B, N, K, d, float(scale),
-            _p(dX), _p(dC), _p(ws), ws.numel(), s))
+            _a(X), _dt(X.dtype), _a(C), _a(ids), _a(lse), _a(g), B, N, K, d, float(scale),
+            _a(dX), _a(dC), _a(ws), ws.numel(), s))
     return dX, dC
 
 

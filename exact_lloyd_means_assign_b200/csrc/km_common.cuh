@@ -84,6 +84,25 @@ __device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool pred
     return r != 0;
 }
 
+// ------------------------------------------------------------------ division by a launch constant
+
+// Quotient by a divisor fixed per launch, for numerators below 2^31:
+// q = (umulhi(m, n) + n) >> s with s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
+struct FastDiv {
+    uint32_t m, s, d;
+};
+inline FastDiv make_fastdiv(uint32_t d) {
+    FastDiv f;
+    f.d = d;
+    f.s = 0;
+    while ((uint64_t{1} << f.s) < d) ++f.s;
+    f.m = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << f.s) - d)) / d + 1);
+    return f;
+}
+__device__ __forceinline__ uint32_t fd_div(const FastDiv &f, uint32_t n) {
+    return (__umulhi(f.m, n) + n) >> f.s;
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

@@ -13,23 +13,6 @@
 namespace km {
 namespace lk {
 
-// Quotient and remainder by a divisor fixed per launch, for numerators below 2^31:
-// q = (umulhi(m, n) + n) >> s with s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1.
-struct FastDiv {
-    uint32_t m, s, d;
-};
-inline FastDiv make_fastdiv(uint32_t d) {
-    FastDiv f;
-    f.d = d;
-    f.s = 0;
-    while ((uint64_t{1} << f.s) < d) ++f.s;
-    f.m = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << f.s) - d)) / d + 1);
-    return f;
-}
-__device__ __forceinline__ uint32_t fd_div(const FastDiv &f, uint32_t n) {
-    return (__umulhi(f.m, n) + n) >> f.s;
-}
-
 // V consecutive elements of T as one access.
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
     T v[V];
@@ -361,6 +344,8 @@ __global__ void __launch_bounds__(kGradThreads)
 namespace {
 
 using namespace km::lk;
+using km::FastDiv;
+using km::make_fastdiv;
 
 inline bool elem_ok(const void *p, km_dtype dt) { return aligned(p, dtype_size(dt)); }
 
