@@ -12,12 +12,16 @@
 #include "kmeans_b200.h"
 
 // The device error word and the wait limit of km_common.cuh exist once per translation unit; the
-// unit of the cross entropy exports its own for km_device_error and km_debug_wait_limit.
+// other units that wait export theirs for km_device_error and km_debug_wait_limit.
 namespace km {
 namespace xe {
 cudaError_t take_device_error(unsigned int *bits);            // reads and clears
 cudaError_t set_wait_limit(unsigned long long limit_ns);
 }  // namespace xe
+namespace mv4 {
+cudaError_t take_device_error(unsigned int *bits);
+cudaError_t set_wait_limit(unsigned long long limit_ns);
+}  // namespace mv4
 }  // namespace km
 
 namespace {

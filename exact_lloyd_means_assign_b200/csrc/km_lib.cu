@@ -1652,9 +1652,10 @@ km_status km_device_error(void *stream, int *code) {
     if (cudaMemcpyFromSymbol(&v, km::g_km_dev_error, sizeof(v)) != cudaSuccess ||
         cudaMemcpyToSymbol(km::g_km_dev_error, &zero, sizeof(zero)) != cudaSuccess)
         return KM_ERR_CUDA;
-    unsigned int other = 0;
-    if (km::xe::take_device_error(&other) != cudaSuccess) return KM_ERR_CUDA;
-    v |= other;
+    unsigned int xe = 0, mv4 = 0;
+    if (km::xe::take_device_error(&xe) != cudaSuccess || km::mv4::take_device_error(&mv4) != cudaSuccess)
+        return KM_ERR_CUDA;
+    v |= xe | mv4;
     *code = static_cast<int>(v);
     return v ? KM_ERR_DEVICE_TIMEOUT : KM_OK;
 }
@@ -1665,7 +1666,7 @@ km_status km_debug_wait_limit(unsigned long long limit_ns, unsigned long long *p
     if (cudaDeviceSynchronize() != cudaSuccess ||
         cudaMemcpyFromSymbol(&old, km::g_km_wait_limit_ns, sizeof(old)) != cudaSuccess ||
         cudaMemcpyToSymbol(km::g_km_wait_limit_ns, &limit_ns, sizeof(limit_ns)) != cudaSuccess ||
-        km::xe::set_wait_limit(limit_ns) != cudaSuccess)
+        km::xe::set_wait_limit(limit_ns) != cudaSuccess || km::mv4::set_wait_limit(limit_ns) != cudaSuccess)
         return KM_ERR_CUDA;
     if (previous_ns) *previous_ns = old;
     return KM_OK;

@@ -91,43 +91,75 @@ __global__ void __launch_bounds__(32 * kSimtWarps)
 
 // ------------------------------------------------------------------ 16-bit tokens: mma form
 //
-// One block per 16 rows of weights. The product runs as m16n8k16 matrix instructions with the weights
+// Tiles of 16 rows of weights. The product runs as m16n8k16 matrix instructions with the weights
 // as the row operand: their rate is far above what the codes' bytes need, so eight tokens cost
 // what one costs, and what bounds the kernel is turning codes into operands. That takes one
 // shared-memory read per pair of codes: a byte indexes a 256-entry table of value pairs. A table
-// row is 128 bytes, one word per lane, so every lane reads its own bank (lane l of a fragment
-// serves rows l / 4 and l / 4 + 8, whose tables are repeated for the four lanes of a row): 32
-// pairs per clock and SM whatever the codes are.
+// row is 256 bytes, one word per lane and row half, so every lane reads its own bank (lane l of a
+// fragment serves rows l / 4 and l / 4 + 8, whose tables are repeated for the four lanes of a
+// row): 32 pairs per clock and SM whatever the codes are. The table starts on a multiple of 64 KB
+// of the shared window, so a single byte permutation of (codes, lane) is the address.
 //
-// Within a block of 4 * CH consecutive codes, lane t of a row holds the CH codes from t * CH on (one
-// vector load), and instruction j multiplies its codes 4j .. 4j + 3 with the same positions of
-// x: the order of the reduction index inside an instruction is free. CH is the largest of 32, 16
-// and 8 for which a block lies in one scale group, so a scale multiplies an fp32 sum, never a
-// weight.
-constexpr int kMmaWarps = 8;
-constexpr int kMmaThreads = 32 * kMmaWarps;
-constexpr uint32_t kTabBytes = 256 * 256;      // [entry][row half][lane] words
+// A block is one per SM and persistent; its two halves of eight warps work on tiles of their own
+// (one builds its table while the other multiplies) and share nothing. The codes come through a
+// ring of TMA copies per half (a stage is four boxes of 16 rows x 128 bytes, requested ahead across
+// tiles), which keeps them off the load pipe that the lookups need; with the 128-byte swizzle the
+// eight rows a warp reads at once lie in different banks. (Plain bulk copies, one per row, took a
+// warp longer to issue than the whole stage takes to multiply.) A pair of
+// instructions multiplies 32 consecutive codes, lane t of a row holding codes 8t .. 8t + 7 (the
+// order of the reduction index inside an instruction is free), so its tokens are one 64-byte
+// piece per row and every scale group of a multiple of 32 codes ends between two pairs: a scale
+// multiplies an fp32 sum, never a weight.
+constexpr int kMmaWarps = 8;                   // per half: each takes 128 codes of a stage's 1024
+constexpr int kHalfThreads = 32 * kMmaWarps;
+constexpr int kMmaThreads = 2 * kHalfThreads + 64;   // and a requesting warp per half
+constexpr uint32_t kTabBytes = 65536;          // [entry][row half][lane] words
+constexpr int kMmaStages = 4;
+constexpr int kStageRow = 512;                 // bytes of a row per stage
+constexpr uint32_t kBoxBytes = 16 * 128;
+constexpr uint32_t kStageBytes = 16 * kStageRow;
+constexpr uint32_t kRingBytes = kMmaStages * kStageBytes;
+// One ring below the 64 KB boundary that the tables start on, one behind the tables.
+constexpr uint32_t kMmaSmem = 3 * kTabBytes + kRingBytes;
 
 struct MmaParams {
-    const uint8_t *packed;
     const float *C, *scales;
     int64_t pitch, R, M;
-    int N, K, ngroups, blocks;   // blocks of 4 * CH codes per row
-    FastDiv bpg;                 // blocks per scale group
-    int xvec;                    // rows of x start on 16-byte boundaries
+    int N, K, ngroups;
+    int rtiles, items;           // tiles of 16 rows, times tiles of 8 NT tokens
+    FastDiv cpg;                 // 32-code chunks per scale group
 };
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+// A word of the tables, which do not change while a tile's lookups run: no memory clobber, the
+// barriers around the tile order the accesses.
+template <int OFF> __device__ __forceinline__ uint32_t lds_tab(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF));
+    return v;
+}
+__device__ __forceinline__ void prefetch_l2(const void *a) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(v) : "memory");
+}
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
 __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 template <>
 __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -135,157 +167,308 @@ template <typename T> __device__ __forceinline__ uint32_t bits16(T v) {
     return *reinterpret_cast<const uint16_t *>(&v);
 }
 
-// CH codes (CH / 8 words) at p.
-template <int CH> struct Codes {
-    uint32_t w[CH / 8];
-};
-template <int CH> __device__ __forceinline__ Codes<CH> load_codes(const uint8_t *p) {
-    Codes<CH> c;
-    if constexpr (CH == 32) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-        c.w[0] = v.x, c.w[1] = v.y, c.w[2] = v.z, c.w[3] = v.w;
-    } else if constexpr (CH == 16) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-        c.w[0] = v.x, c.w[1] = v.y;
+// One token's values of eight consecutive positions, zeros past the end of the row.
+template <typename T, bool XV>
+__device__ __forceinline__ void load_x(const T *xr, int at, int N, uint32_t (&b)[4]) {
+    if (XV) {              // rows are whole 16-byte units
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (at < N) v = __ldg(reinterpret_cast<const uint4 *>(xr + at));
+        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
     } else {
-        c.w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[i] = 0;
+            if (at + 2 * i < N) b[i] = bits16(xr[at + 2 * i]);
+            if (at + 2 * i + 1 < N) b[i] |= bits16(xr[at + 2 * i + 1]) << 16;
+        }
     }
-    return c;
 }
 
-template <typename T, int CH, int NT>
-__global__ void __launch_bounds__(kMmaThreads, NT == 1 ? 3 : 2)
-    matvec4_mma_kernel(const T *__restrict__ x, const MmaParams p, T *__restrict__ y) {
-    extern __shared__ __align__(16) uint8_t tab[];
-    __shared__ float red[kMmaWarps][16][8 * NT + 1];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t = lane & 3;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 16;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (8 * NT);
-    // rows behind the last one repeat it; their sums are not written
-    const int64_t ra = min(r0 + g, p.R - 1), rb = min(r0 + g + 8, p.R - 1);
-    const uint8_t *pa = p.packed + ra * p.pitch, *pb = p.packed + rb * p.pitch;
-    const int chunk0 = t * CH;
-    auto in_row = [&](int blk) { return blk < p.blocks && blk * (4 * CH) + chunk0 < p.N; };
-    Codes<CH> ca = {}, cb = {};
-    if (in_row(warp)) {
-        ca = load_codes<CH>(pa + (static_cast<int64_t>(warp) * (4 * CH) + chunk0) / 2);
-        cb = load_codes<CH>(pb + (static_cast<int64_t>(warp) * (4 * CH) + chunk0) / 2);
+// Warp-wide bounded wait whose waiting part is kept out of the loops it is used in.
+__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return mbar_wait_warp(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    return mbar_wait_long(bar, parity, abort_flag);
+}
+
+// SC: 0 no scales, 1 groups of whole 128-code blocks, 2 any multiple of 32.
+template <typename T, bool XV, int NT, int SC>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    matvec4_mma_kernel(const __grid_constant__ CUtensorMap tm, const T *__restrict__ x, const MmaParams p,
+                       T *__restrict__ y) {
+    constexpr int XD = NT > 2 ? 2 : 4;       // chunks of tokens held ahead
+    constexpr int kCodesPerStage = 2 * kStageRow;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[2][2 * kMmaStages];
+    __shared__ __align__(16) uint16_t values[2][16][24];   // the tile's codebooks (rows 48 bytes apart)
+    __shared__ int abort_flags[2];
+    const uint32_t base = smem_u32(smem);
+    const uint32_t tab0 = (base + 1024 + kRingBytes + kTabBytes - 1) & ~(kTabBytes - 1);
+    if (tab0 + 2 * kTabBytes + kRingBytes > base + kMmaSmem) {   // never: the window starts near 0
+        if (threadIdx.x == 0) record_dev_error(kDevErrTimeout);
+        return;
     }
-    {
-        // pair tables: this thread's row, the 16 entries with high code `hi`
-        const int row = threadIdx.x & 15, hi = threadIdx.x >> 4;
-        const float *Cr = p.C + min(r0 + row, p.R - 1) * p.K;
-        uint32_t v[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = k < p.K ? bits16(Cvt<T>::from_f(Cr[k])) : 0u;
-        uint32_t vh = 0;
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-            if (k == hi) vh = v[k] << 16;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const uint32_t e = v[k] | vh;
-            *reinterpret_cast<uint4 *>(tab + (hi * 16 + k) * 256 + (row >> 3) * 128 + (row & 7) * 16) = make_uint4(e, e, e, e);
+    const int lane = threadIdx.x & 31;
+    const bool producer = threadIdx.x >= 2 * kHalfThreads;
+    const int half = producer ? (threadIdx.x - 2 * kHalfThreads) >> 5 : threadIdx.x / kHalfThreads;
+    const uint32_t ring = half ? tab0 + 2 * kTabBytes : (base + 1023) & ~1023u;
+    const uint32_t full0 = smem_u32(bars[half]), empty0 = full0 + 8 * kMmaStages;
+    volatile int *abortp = &abort_flags[half];
+    const int nstages = static_cast<int>((p.pitch + kStageRow - 1) / kStageRow);
+    if (threadIdx.x < 2) {
+        abort_flags[threadIdx.x] = 0;
+        const uint32_t b = smem_u32(bars[threadIdx.x]);
+        for (int s = 0; s < kMmaStages; ++s) {
+            mbar_init(b + 8 * s, 1);
+            mbar_init(b + 8 * (kMmaStages + s), kMmaWarps);
         }
+        fence_mbar_init();
     }
     __syncthreads();
-    float tot[NT][4];
+    const int item0 = half * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x), step = 2 * static_cast<int>(gridDim.x);
+
+    if (producer) {
+        // Requests the stages of the half's tiles one after the other. Rows and bytes behind the end
+        // arrive as zeros.
+        const uint64_t pol = l2_policy_evict_first();
+        int slot = 0, asked = 0;
+        uint32_t ph = 1;
+        for (int item = item0; item < p.items; item += step) {
+            const int row = (item % p.rtiles) * 16;
+            for (int s = 0; s < nstages; ++s) {
+                if (!mbar_wait_warp(empty0 + 8 * slot, ph, abortp)) { item = p.items - step; break; }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full0 + 8 * slot, kStageBytes);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tot[n][i] = 0.f;
-    const T *xr[NT];
-    bool xin[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        xin[n] = m0 + n * 8 + g < p.M;
-        xr[n] = x + (m0 + n * 8 + g) * p.N;
+                    for (int i = 0; i < kStageRow / 128; ++i)
+                        tma_load_2d(ring + slot * kStageBytes + i * kBoxBytes, &tm, full0 + 8 * slot, s * kStageRow + i * 128,
+                                    row, pol);
+                }
+                __syncwarp();
+                ++asked;
+                if (++slot == kMmaStages) { slot = 0; ph ^= 1u; }
+            }
+        }
+        // every copy lands before its memory goes away, after a wait that ran out too
+        for (int s = max(0, asked - kMmaStages); s < asked; ++s)
+            mbar_wait_warp(full0 + 8 * (s % kMmaStages), (s / kMmaStages) & 1, nullptr);
+        return;
     }
-    const uint32_t lane4 = lane * 4;
-    const float *sa = p.scales ? p.scales + ra * p.ngroups : nullptr, *sb = p.scales ? p.scales + rb * p.ngroups : nullptr;
-    for (int blk = warp; blk < p.blocks; blk += kMmaWarps) {
-        const int n0 = blk * (4 * CH) + chunk0;
-        const Codes<CH> a = ca, b = cb;
-        if (in_row(blk + kMmaWarps)) {
-            ca = load_codes<CH>(pa + (static_cast<int64_t>(blk + kMmaWarps) * (4 * CH) + chunk0) / 2);
-            cb = load_codes<CH>(pb + (static_cast<int64_t>(blk + kMmaWarps) * (4 * CH) + chunk0) / 2);
+
+    const int ht = threadIdx.x % kHalfThreads, warp = ht >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t tab = tab0 + half * kTabBytes;
+    // Codebook value ht % 16 of row ht / 16 of an item's tile (0 beyond the codebook or the rows).
+    auto codebook_value = [&](int item) {
+        const int64_t row = static_cast<int64_t>(item % p.rtiles) * 16 + (ht >> 4);
+        return item < p.items && row < p.R && (ht & 15) < p.K ? __ldg(p.C + row * p.K + (ht & 15)) : 0.f;
+    };
+    float cval = codebook_value(item0);
+    const uint32_t lane4 = tab + lane * 4;                    // byte 0 the lane's word, 2-3 the table
+    // this lane's word of chunk h: 16-byte unit (warp % 2) * 4 + h of row g (or g + 8) in box warp / 2,
+    // swizzled: unit u of row r lies at u ^ (r % 8)
+    const uint32_t my_codes = ring + (warp >> 1) * kBoxBytes + g * 128 + t * 4;
+    const uint32_t unit0 = (((warp & 1) * 4) ^ g) * 16;       // of chunk h: unit0 ^ 16 h
+    int slot = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int item = item0; item < p.items; item += step) {
+        const int64_t r0 = static_cast<int64_t>(item % p.rtiles) * 16;
+        const int64_t m0 = static_cast<int64_t>(item / p.rtiles) * (8 * NT);
+        // Lanes without a token load nothing and multiply whatever they hold: columns do not mix,
+        // and theirs are not written. (A 16-byte load costs the load pipe a cycle per eight lanes
+        // even where all lanes name the same address.)
+        const T *xr[NT];       // this lane's positions of the warp's block in the current stage
+        bool xin[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            xin[n] = m0 + n * 8 + g < p.M;
+            xr[n] = x + min(m0 + n * 8 + g, p.M - 1) * p.N + warp * 128 + t * 8;
         }
-        float s0 = 1.f, s1 = 1.f;
-        if (sa) {
-            const int gi = fd_div(p.bpg, blk);
-            s0 = sa[gi];
-            s1 = sb[gi];
+        const float *sa = nullptr, *sb = nullptr;
+        if (SC) {
+            sa = p.scales + min(r0 + g, p.R - 1) * p.ngroups;
+            sb = p.scales + min(r0 + g + 8, p.R - 1) * p.ngroups;
         }
-        const bool whole = (blk + 1) * (4 * CH) <= p.N;      // the same for the whole warp
-        float acc[NT][4];
+        const int nfull = p.N / kCodesPerStage;
+        // Tokens and scales are read one stage ahead: chunk h of the next stage replaces chunk h of
+        // this one as soon as that is multiplied (after the last stage it is read again).
+        uint32_t xb[XD][NT][4];
+#pragma unroll
+        for (int h = 0; h < XD; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xb[h][n][i] = 0;
+        auto next_x = [&](int h, int add, int b) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (!xin[n]) continue;
+                if (XV) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(xr[n] + add + h * 32));
+                    xb[b][n][0] = v.x, xb[b][n][1] = v.y, xb[b][n][2] = v.z, xb[b][n][3] = v.w;
+                } else {
+                    load_x<T, false>(xr[n] + add + h * 32, 0, 8, xb[b][n]);
+                }
+            }
+        };
+        // The four lanes of a row hold four of its scales each time: those of the warp's blocks in
+        // four consecutive stages (SC 1) or of the four chunks of its block (SC 2).
+        float sca = 1.f, scb = 1.f, nxa = 1.f, nxb = 1.f;
+        auto read_scales = [&](int s, float &a, float &b) {
+            const uint32_t q = SC == 1 ? (min(s + t, nfull - 1) * kMmaWarps + warp) * 4 : (s * kMmaWarps + warp) * 4 + t;
+            const uint32_t gi = fd_div(p.cpg, q);
+            a = __ldg(sa + gi);
+            b = __ldg(sb + gi);
+        };
+        if (nfull > 0) {
+#pragma unroll
+            for (int h = 0; h < XD; ++h) next_x(h, 0, h);
+            if (SC) read_scales(0, nxa, nxb);
+        }
+        {
+            // pair tables: this thread's row, the 16 entries with high code `hi`; every thread holds
+            // one codebook value of the tile, read while the tile before was multiplied
+            values[half][ht >> 4][ht & 15] = bits16(Cvt<T>::from_f(cval));
+            named_barrier_sync(1 + half, kHalfThreads);       // and the previous tile's sums are read
+            cval = codebook_value(item + step);
+            if (SC) {
+                // the next tile's scales into L2
+                const int64_t r1 = static_cast<int64_t>((item + step) % p.rtiles) * 16 + (ht >> 4);
+                if (item + step < p.items && r1 < p.R)
+                    for (int o = (ht & 15) * 32; o < p.ngroups; o += 512) prefetch_l2(p.scales + r1 * p.ngroups + o);
+            }
+            const int row = ht & 15, hi = ht >> 4;
+            const uint4 c0 = *reinterpret_cast<const uint4 *>(&values[half][row][0]);
+            const uint4 c1 = *reinterpret_cast<const uint4 *>(&values[half][row][8]);
+            const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+            const uint32_t vh = static_cast<uint32_t>(values[half][row][hi]) << 16;
+            const uint32_t dst = tab + hi * 4096 + (row >> 3) * 128 + (row & 7) * 16;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+                sts128(dst + k * 256, __byte_perm(c[k / 2], vh, 0x7610));
+                sts128(dst + k * 256 + 256, __byte_perm(c[k / 2], vh, 0x7632));
+            }
+        }
+        named_barrier_sync(1 + half, kHalfThreads);
+        float tot[NT][4], acc[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-#pragma unroll
-        for (int h = 0; h < CH / 8; ++h) {       // eight codes, two instructions
-            uint32_t xb[NT][4];
+            for (int i = 0; i < 4; ++i) tot[n][i] = acc[n][i] = 0.f;
+        auto add = [&](float a0, float a1) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int at = n0 + h * 8;
+                tot[n][0] = fmaf(a0, acc[n][0], tot[n][0]);
+                tot[n][1] = fmaf(a0, acc[n][1], tot[n][1]);
+                tot[n][2] = fmaf(a1, acc[n][2], tot[n][2]);
+                tot[n][3] = fmaf(a1, acc[n][3], tot[n][3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xb[n][i] = 0;
-                if (xin[n]) {
-                    if (whole && p.xvec) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(xr[n] + at));
-                        xb[n][0] = v.x, xb[n][1] = v.y, xb[n][2] = v.z, xb[n][3] = v.w;
-                    } else {
+                for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+            }
+        };
+        // the four operand words of instruction j of a pair
+        auto operand = [&](uint32_t wa, uint32_t wb, int j, uint32_t (&f)[4]) {
+            const uint32_t k0 = 0x7604 | (2 * j) << 4, k1 = 0x7604 | (2 * j + 1) << 4;
+            f[0] = lds_tab<0>(__byte_perm(wa, lane4, k0));
+            f[1] = lds_tab<128>(__byte_perm(wb, lane4, k0));
+            f[2] = lds_tab<0>(__byte_perm(wa, lane4, k1));
+            f[3] = lds_tab<128>(__byte_perm(wb, lane4, k1));
+        };
+#pragma unroll 1
+        for (int s = 0; s < nfull; ++s) {
+            if (!mbar_ready(full0 + 8 * slot, ph, abortp)) { ok = false; break; }
+            uint32_t wa[4], wb[4];
+            {
+                const uint32_t src = my_codes + slot * kStageBytes + unit0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (at + 2 * i < p.N) xb[n][i] = bits16(xr[n][at + 2 * i]);
-                            if (at + 2 * i + 1 < p.N) xb[n][i] |= bits16(xr[n][at + 2 * i + 1]) << 16;
-                        }
-                    }
+                for (int h = 0; h < 4; ++h) {
+                    // (unit0 ^ 16 h) == unit0 +- 16 h bit by bit: xor on the address, whose bits 4-6 it is
+                    wa[h] = lds32(src ^ (h * 16));
+                    wb[h] = lds32((src ^ (h * 16)) + 8 * 128);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t f[4];
-                // table offset of a byte: the byte as bits 8-15, the lane's word below it
-                f[0] = *reinterpret_cast<const uint32_t *>(tab + __byte_perm(a.w[h], lane4, 0x7704 | (2 * j) << 4));
-                f[1] = *reinterpret_cast<const uint32_t *>(tab + 128 + __byte_perm(b.w[h], lane4, 0x7704 | (2 * j) << 4));
-                f[2] = *reinterpret_cast<const uint32_t *>(tab + __byte_perm(a.w[h], lane4, 0x7704 | (2 * j + 1) << 4));
-                f[3] = *reinterpret_cast<const uint32_t *>(tab + 128 + __byte_perm(b.w[h], lane4, 0x7704 | (2 * j + 1) << 4));
-                if (!whole) {
-                    // codes behind the row's end are no weights (a codebook value may be infinite)
-                    const int at = n0 + h * 8 + 4 * j;
-                    if (at >= p.N) f[0] = f[1] = 0;
-                    else if (at + 1 >= p.N) f[0] &= 0xffff, f[1] &= 0xffff;
-                    if (at + 2 >= p.N) f[2] = f[3] = 0;
-                    else if (at + 3 >= p.N) f[2] &= 0xffff, f[3] &= 0xffff;
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816<T>(acc[n], f, xb[n][2 * j], xb[n][2 * j + 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * slot);
+            const int ahead = s + 1 < nfull ? kCodesPerStage : 0;
+            if (SC == 2 || (SC == 1 && (s & 3) == 0)) {
+                sca = nxa, scb = nxb;
+                const int ns = s + (SC == 1 ? 4 : 1);
+                if (ns < nfull) read_scales(ns, nxa, nxb);
             }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t f[4];
+                    operand(wa[h], wb[h], j, f);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma16816<T>(SC ? acc[n] : tot[n], f, xb[h % XD][n][2 * j], xb[h % XD][n][2 * j + 1]);
+                }
+                if (h + XD < 4) next_x(h + XD, 0, h % XD);
+                else next_x(h + XD - 4, ahead, h % XD);
+                if (SC == 2) add(__shfl_sync(0xffffffffu, sca, (lane & 28) + h), __shfl_sync(0xffffffffu, scb, (lane & 28) + h));
+            }
+            if (SC == 1) add(__shfl_sync(0xffffffffu, sca, (lane & 28) + (s & 3)), __shfl_sync(0xffffffffu, scb, (lane & 28) + (s & 3)));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) xr[n] += kCodesPerStage;
+            if (++slot == kMmaStages) { slot = 0; ph ^= 1u; }
         }
+        if (ok && nfull < nstages) {
+            // the last, partly filled stage
+            if (!mbar_ready(full0 + 8 * slot, ph, abortp)) ok = false;
+            const uint32_t src = my_codes + slot * kStageBytes + unit0;
+            const int q0 = (nfull * kMmaWarps + warp) * 4;
+            for (int h = 0; ok && h < 4 && (q0 + h) * 32 < p.N; ++h) {
+                const int at = (q0 + h) * 32 + 8 * t;        // this lane's first code
+                uint32_t xt[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) load_x<T, XV>(xr[n] + h * 32, 0, xin[n] ? p.N - at : 0, xt[n]);
+                const uint32_t wa = lds32(src ^ (h * 16)), wb = lds32((src ^ (h * 16)) + 8 * 128);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t f[4];
+                    operand(wa, wb, j, f);
+                    // codes behind the row's end are no weights (a codebook value may be infinite)
+                    const int c = at + 4 * j;
+                    if (c >= p.N) f[0] = f[1] = 0;
+                    else if (c + 1 >= p.N) f[0] &= 0xffff, f[1] &= 0xffff;
+                    if (c + 2 >= p.N) f[2] = f[3] = 0;
+                    else if (c + 3 >= p.N) f[2] &= 0xffff, f[3] &= 0xffff;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16816<T>(SC ? acc[n] : tot[n], f, xt[n][2 * j], xt[n][2 * j + 1]);
+                }
+                if (SC) {
+                    const uint32_t gi = fd_div(p.cpg, q0 + h);
+                    add(sa[gi], sb[gi]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * slot);
+            if (++slot == kMmaStages) { slot = 0; ph ^= 1u; }
+        }
+        // the warps' sums, joined in warp order, through the table's place: [warp][token][17]
+        if (named_barrier_or(1 + half, kHalfThreads, !ok)) break;
+        float *red = reinterpret_cast<float *>(smem + (tab - base));
+        float *w = red + warp * (8 * NT * 17);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            tot[n][0] = fmaf(s0, acc[n][0], tot[n][0]);
-            tot[n][1] = fmaf(s0, acc[n][1], tot[n][1]);
-            tot[n][2] = fmaf(s1, acc[n][2], tot[n][2]);
-            tot[n][3] = fmaf(s1, acc[n][3], tot[n][3]);
+            w[(n * 8 + 2 * t) * 17 + g] = tot[n][0];
+            w[(n * 8 + 2 * t + 1) * 17 + g] = tot[n][1];
+            w[(n * 8 + 2 * t) * 17 + g + 8] = tot[n][2];
+            w[(n * 8 + 2 * t + 1) * 17 + g + 8] = tot[n][3];
         }
-    }
+        named_barrier_sync(1 + half, kHalfThreads);
+        for (int i = ht; i < 16 * 8 * NT; i += kHalfThreads) {
+            const int r = i & 15, mm = i >> 4;
+            float v = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        red[warp][g][n * 8 + 2 * t] = tot[n][0];
-        red[warp][g][n * 8 + 2 * t + 1] = tot[n][1];
-        red[warp][g + 8][n * 8 + 2 * t] = tot[n][2];
-        red[warp][g + 8][n * 8 + 2 * t + 1] = tot[n][3];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * 8 * NT; i += kMmaThreads) {
-        const int r = i & 15, m = i >> 4;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w) v += red[w][r][m];
-        if (r0 + r < p.R && m0 + m < p.M) y[(m0 + m) * p.R + r0 + r] = Cvt<T>::from_f(v);
+            for (int k = 0; k < kMmaWarps; ++k) v += red[k * (8 * NT * 17) + mm * 17 + r];
+            if (r0 + r < p.R && m0 + mm < p.M) y[(m0 + mm) * p.R + r0 + r] = Cvt<T>::from_f(v);
+        }
     }
 }
 
@@ -314,36 +497,59 @@ km_status matvec4_simt(const void *xv, int64_t M, const uint8_t *packed, const f
     return launch_status();
 }
 
-template <typename T, int CH, int NT>
-km_status mma_launch(const T *x, MmaParams p, T *y, cudaStream_t st) {
-    auto kernel = matvec4_mma_kernel<T, CH, NT>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTabBytes)) !=
-        cudaSuccess)
-        return KM_ERR_CUDA;
-    // token tiles beyond the grid's y extent in further launches
-    const int64_t per = static_cast<int64_t>(kMaxGridY) * 8 * NT, M = p.M;
+template <typename T, bool XV, int NT, int SC>
+km_status mma_launch(const CUtensorMap &tm, const T *x, MmaParams p, T *y, cudaStream_t st) {
+    auto kernel = matvec4_mma_kernel<T, XV, NT, SC>;
+    static bool ready[64] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !ready[dev]) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMmaSmem)) !=
+            cudaSuccess)
+            return KM_ERR_CUDA;
+        if (dev >= 0 && dev < 64) ready[dev] = true;
+    }
+    const int64_t rtiles = ceil_div(p.R, 16);
+    if (rtiles > kMaxIndex / 4) return KM_ERR_UNSUPPORTED;
+    // as many token tiles per launch as keep the item number below 2^30
+    const int64_t per = std::max<int64_t>(1, (int64_t{1} << 30) / rtiles) * 8 * NT, M = p.M;
     for (int64_t m0 = 0; m0 < M; m0 += per) {
         p.M = std::min(per, M - m0);
-        const dim3 grid(static_cast<unsigned>(ceil_div(p.R, 16)), static_cast<unsigned>(ceil_div(p.M, 8 * NT)));
-        kernel<<<grid, kMmaThreads, kTabBytes, st>>>(x + m0 * p.N, p, y + m0 * p.R);
+        p.rtiles = static_cast<int>(rtiles);
+        p.items = static_cast<int>(rtiles * ceil_div(p.M, 8 * NT));
+        kernel<<<static_cast<unsigned>(std::min(p.items, num_sms())), kMmaThreads, kMmaSmem, st>>>(
+            tm, x + m0 * p.N, p, y + m0 * p.R);
         if (launch_status() != KM_OK) return KM_ERR_CUDA;
     }
     return KM_OK;
 }
-template <typename T, int CH>
-km_status mma_tokens(const T *x, MmaParams p, T *y, cudaStream_t st) {
-    p.blocks = static_cast<int>(ceil_div(p.N, 4 * CH));
-    if (p.M <= 8) return mma_launch<T, CH, 1>(x, p, y, st);
-    if (p.M <= 16) return mma_launch<T, CH, 2>(x, p, y, st);
-    return mma_launch<T, CH, 4>(x, p, y, st);
+template <typename T, bool XV, int SC>
+km_status mma_tokens(const CUtensorMap &tm, const T *x, const MmaParams &p, T *y, cudaStream_t st) {
+    if (p.M <= 8) return mma_launch<T, XV, 1, SC>(tm, x, p, y, st);
+    if (p.M <= 16) return mma_launch<T, XV, 2, SC>(tm, x, p, y, st);
+    return mma_launch<T, XV, 4, SC>(tm, x, p, y, st);
+}
+template <typename T, bool XV>
+km_status mma_scales(const CUtensorMap &tm, const T *x, const MmaParams &p, T *y, cudaStream_t st) {
+    if (!p.scales) return mma_tokens<T, XV, 0>(tm, x, p, y, st);
+    return p.cpg.d % 4 == 0 ? mma_tokens<T, XV, 1>(tm, x, p, y, st) : mma_tokens<T, XV, 2>(tm, x, p, y, st);
 }
 template <typename T>
 km_status matvec4_mma(const void *xv, int64_t M, const uint8_t *packed, const float *C, int64_t R, int64_t N,
                       int64_t K, const float *scales, int64_t group, void *yv, cudaStream_t st) {
     const T *x = static_cast<const T *>(xv);
     T *y = static_cast<T *>(yv);
+    const EncodeTiledFn enc = encode_fn();
+    if (!enc) return KM_ERR_CUDA;
+    CUtensorMap tm;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(pitch_of(N)), static_cast<cuuint64_t>(R)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_of(N))};
+    const cuuint32_t box[2] = {128, 16}, estr[2] = {1, 1};
+    if (enc(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(packed), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return KM_ERR_CUDA;
     MmaParams p = {};
-    p.packed = packed;
     p.C = C;
     p.scales = scales;
     p.pitch = pitch_of(N);
@@ -352,17 +558,26 @@ km_status matvec4_mma(const void *xv, int64_t M, const uint8_t *packed, const fl
     p.N = static_cast<int>(N);
     p.K = static_cast<int>(K);
     p.ngroups = scales ? static_cast<int>(ceil_div(N, group)) : 0;
-    p.xvec = N % 8 == 0 && aligned(x, 16) ? 1 : 0;
-    const int ch = !scales || group % 128 == 0 ? 32 : group % 64 == 0 ? 16 : 8;
-    p.bpg = km::make_fastdiv(static_cast<uint32_t>(scales ? group / (4 * ch) : 1));
-    switch (ch) {
-        case 32: return mma_tokens<T, 32>(x, p, y, st);
-        case 16: return mma_tokens<T, 16>(x, p, y, st);
-        default: return mma_tokens<T, 8>(x, p, y, st);
-    }
+    p.cpg = km::make_fastdiv(static_cast<uint32_t>(scales ? group / 32 : 4));
+    return N % 8 == 0 && aligned(x, 16) ? mma_scales<T, true>(tm, x, p, y, st) : mma_scales<T, false>(tm, x, p, y, st);
 }
 
 }  // namespace
+
+namespace km {
+namespace mv4 {
+
+cudaError_t take_device_error(unsigned int *bits) {
+    const unsigned int zero = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(bits, g_km_dev_error, sizeof(*bits));
+    return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_km_dev_error, &zero, sizeof(zero));
+}
+cudaError_t set_wait_limit(unsigned long long limit_ns) {
+    return cudaMemcpyToSymbol(g_km_wait_limit_ns, &limit_ns, sizeof(limit_ns));
+}
+
+}  // namespace mv4
+}  // namespace km
 
 extern "C" {
 
