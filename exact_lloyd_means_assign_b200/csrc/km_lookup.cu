@@ -17,50 +17,92 @@ namespace lk {
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec {
     T v[V];
 };
+template <typename T, int V> __device__ __forceinline__ Vec<T, V> load_ro(const Vec<T, V> *p) {
+    constexpr int kBytes = sizeof(T) * V;
+    Vec<T, V> r;
+    if constexpr (kBytes == 16) *reinterpret_cast<uint4 *>(&r) = __ldg(reinterpret_cast<const uint4 *>(p));
+    else if constexpr (kBytes == 8) *reinterpret_cast<uint2 *>(&r) = __ldg(reinterpret_cast<const uint2 *>(p));
+    else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t *>(&r) = __ldg(reinterpret_cast<const uint32_t *>(p));
+    else *reinterpret_cast<uint16_t *>(&r) = __ldg(reinterpret_cast<const uint16_t *>(p));
+    return r;
+}
+
+// Streaming store: the result is written once and would only push the table out of L2.
+template <typename T, int V> __device__ __forceinline__ void store_cs(Vec<T, V> *p, Vec<T, V> r) {
+    constexpr int kBytes = sizeof(T) * V;
+    if constexpr (kBytes == 16) __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<uint4 *>(&r));
+    else if constexpr (kBytes == 8) __stcs(reinterpret_cast<uint2 *>(p), *reinterpret_cast<uint2 *>(&r));
+    else if constexpr (kBytes == 4) __stcs(reinterpret_cast<uint32_t *>(p), *reinterpret_cast<uint32_t *>(&r));
+    else __stcs(reinterpret_cast<uint16_t *>(p), *reinterpret_cast<uint16_t *>(&r));
+}
 
 // ------------------------------------------------------------------ lookup
 
 constexpr int kLookupThreads = 256;
 
-// TPR threads per row (a power of two), each moving units of V elements; kRows rows per thread
-// group so that several table reads are in flight.
-template <typename T, int V, int TPR, int ROWS>
+// A warp serves `rpw` consecutive rows (at most 32): each lane finds one row's source once, then
+// the rows are moved 32 / TPR at a time, TPR lanes (a power of two) per row and V elements per lane,
+// with 2 rows (4 pieces of a wide row) in flight
+// per lane: more registers per thread cost more in resident warps than they hide (8: 122 us, 4: 91,
+// 2: 87 for 2M rows of 256 bytes). Off is the type of offsets counted in units of V elements: 32 bits
+// wherever table and output have fewer units than 2^32, which halves the address arithmetic that
+// otherwise costs more than the conversion of the values.
+template <typename T, int V, int TPR, typename Off>
 __global__ void __launch_bounds__(kLookupThreads)
     lookup_kernel(const T *__restrict__ C, const int32_t *__restrict__ ids, uint32_t rows, FastDiv divN,
-                  int K, int d, float scale, T *__restrict__ Y) {
-    constexpr int GROUPS = kLookupThreads / TPR;
-    const int g = threadIdx.x / TPR, t = threadIdx.x % TPR;
-    const uint32_t r0 = blockIdx.x * static_cast<uint32_t>(GROUPS * ROWS) + g;
-    const T *src[ROWS];
-    bool in[ROWS];
-#pragma unroll
-    for (int j = 0; j < ROWS; ++j) {
-        const uint32_t r = r0 + j * GROUPS;
-        in[j] = r < rows;
-        src[j] = nullptr;
-        if (in[j]) {
-            const int id = ids[r];
-            const int64_t b = fd_div(divN, r);
-            if (id >= 0 && id < K) src[j] = C + (b * K + id) * d;
-        }
+                  uint32_t K, uint32_t units, int rpw, float scale, T *__restrict__ Y) {
+    constexpr int RS = 32 / TPR, U = 2, UW = 4;
+    constexpr Off kNone = ~Off(0);
+    using Unit = Vec<T, V>;
+    const int lane = threadIdx.x & 31, sub = lane / TPR, t = lane % TPR;
+    const uint32_t row0 = (blockIdx.x * (kLookupThreads / 32) + (threadIdx.x >> 5)) * static_cast<uint32_t>(rpw);
+    if (row0 >= rows) return;
+    const int n = min(static_cast<uint32_t>(rpw), rows - row0);
+    Off src = kNone;
+    if (lane < n) {
+        const uint32_t id = static_cast<uint32_t>(ids[row0 + lane]);
+        if (id < K) src = (static_cast<Off>(fd_div(divN, row0 + lane)) * K + id) * units;
     }
-    for (int c = t * V; c < d; c += TPR * V) {
-        Vec<T, V> v[ROWS];
+    const Unit *Cu = reinterpret_cast<const Unit *>(C);
+    Unit *Yu = reinterpret_cast<Unit *>(Y) + static_cast<Off>(row0) * units;
+    auto scaled = [&](Unit v) {
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-            if (src[j]) {
-                v[j] = *reinterpret_cast<const Vec<T, V> *>(src[j] + c);
+        for (int i = 0; i < V; ++i) v.v[i] = Cvt<T>::from_f(scale * Cvt<T>::to_f(v.v[i]));
+        return v;
+    };
+    Unit zero;
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[j].v[i] = Cvt<T>::from_f(scale * Cvt<T>::to_f(v[j].v[i]));
-            } else {
+    for (int i = 0; i < V; ++i) zero.v[i] = Cvt<T>::from_f(0.f);
+    if (TPR < 32 || units <= 32) {
+        const bool in = t < static_cast<int>(units);
+        for (int j = 0; j < n; j += RS * U) {
+            Unit v[U];
+            Off s[U];
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[j].v[i] = Cvt<T>::from_f(0.f);
+            for (int u = 0; u < U; ++u) {
+                s[u] = __shfl_sync(0xffffffffu, src, (j + u * RS + sub) & 31);
+                if (j + u * RS + sub < n && in && s[u] != kNone) v[u] = load_ro(Cu + s[u] + t);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = j + u * RS + sub;
+                if (r < n && in) store_cs(Yu + static_cast<Off>(r) * units + t, s[u] != kNone ? scaled(v[u]) : zero);
             }
         }
+    } else {
+        for (int j = 0; j < n; ++j) {
+            const Off s = __shfl_sync(0xffffffffu, src, j);
+            Unit *out = Yu + static_cast<Off>(j) * units;
+            for (uint32_t c = t; c < units; c += 32 * UW) {
+                Unit v[UW];
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j)
-            if (in[j])
-                *reinterpret_cast<Vec<T, V> *>(Y + static_cast<int64_t>(r0 + j * GROUPS) * d + c) = v[j];
+                for (int u = 0; u < UW; ++u)
+                    if (c + u * 32 < units && s != kNone) v[u] = load_ro(Cu + s + c + u * 32);
+#pragma unroll
+                for (int u = 0; u < UW; ++u)
+                    if (c + u * 32 < units) store_cs(out + c + u * 32, s != kNone ? scaled(v[u]) : zero);
+            }
+        }
     }
 }
 
@@ -364,25 +406,33 @@ inline int pow2_at_least(int64_t x, int cap) {
 }
 
 template <typename T, int V, int TPR>
-km_status lookup_launch(const T *C, const int32_t *ids, uint32_t rows, FastDiv dv, int K, int d, float scale,
-                        T *Y, cudaStream_t st) {
-    constexpr int ROWS = 4;
-    constexpr int per = kLookupThreads / TPR * ROWS;
-    lookup_kernel<T, V, TPR, ROWS><<<static_cast<unsigned>(ceil_div(rows, per)), kLookupThreads, 0, st>>>(
-        C, ids, rows, dv, K, d, scale, Y);
+km_status lookup_launch(const T *C, const int32_t *ids, uint32_t rows, FastDiv dv, int64_t table_rows, int K, int d,
+                        float scale, T *Y, cudaStream_t st) {
+    // rows per warp: 32 lets every lane look one id up, fewer where that would leave SMs without
+    // warps (16 warps per SM wanted)
+    int rpw = 32;
+    while (rpw > 32 / TPR && ceil_div(rows, rpw) < 148 * 16) rpw /= 2;
+    const unsigned grid = static_cast<unsigned>(ceil_div(ceil_div(rows, rpw), kLookupThreads / 32));
+    const uint32_t units = static_cast<uint32_t>(d / V);
+    constexpr int64_t kMax32 = (int64_t{1} << 32) - 1;
+    if (table_rows * units < kMax32 && static_cast<int64_t>(rows) * units < kMax32)
+        lookup_kernel<T, V, TPR, uint32_t><<<grid, kLookupThreads, 0, st>>>(C, ids, rows, dv, static_cast<uint32_t>(K),
+                                                                            units, rpw, scale, Y);
+    else
+        lookup_kernel<T, V, TPR, uint64_t><<<grid, kLookupThreads, 0, st>>>(C, ids, rows, dv, static_cast<uint32_t>(K),
+                                                                            units, rpw, scale, Y);
     return launch_status();
 }
 template <typename T, int V>
-km_status lookup_tpr(const T *C, const int32_t *ids, uint32_t rows, FastDiv dv, int K, int d, float scale, T *Y,
-                     cudaStream_t st) {
-    switch (pow2_at_least(ceil_div(d, V), 64)) {
-        case 1: return lookup_launch<T, V, 1>(C, ids, rows, dv, K, d, scale, Y, st);
-        case 2: return lookup_launch<T, V, 2>(C, ids, rows, dv, K, d, scale, Y, st);
-        case 4: return lookup_launch<T, V, 4>(C, ids, rows, dv, K, d, scale, Y, st);
-        case 8: return lookup_launch<T, V, 8>(C, ids, rows, dv, K, d, scale, Y, st);
-        case 16: return lookup_launch<T, V, 16>(C, ids, rows, dv, K, d, scale, Y, st);
-        case 32: return lookup_launch<T, V, 32>(C, ids, rows, dv, K, d, scale, Y, st);
-        default: return lookup_launch<T, V, 64>(C, ids, rows, dv, K, d, scale, Y, st);
+km_status lookup_tpr(const T *C, const int32_t *ids, uint32_t rows, FastDiv dv, int64_t tr, int K, int d, float scale,
+                     T *Y, cudaStream_t st) {
+    switch (pow2_at_least(ceil_div(d, V), 32)) {
+        case 1: return lookup_launch<T, V, 1>(C, ids, rows, dv, tr, K, d, scale, Y, st);
+        case 2: return lookup_launch<T, V, 2>(C, ids, rows, dv, tr, K, d, scale, Y, st);
+        case 4: return lookup_launch<T, V, 4>(C, ids, rows, dv, tr, K, d, scale, Y, st);
+        case 8: return lookup_launch<T, V, 8>(C, ids, rows, dv, tr, K, d, scale, Y, st);
+        case 16: return lookup_launch<T, V, 16>(C, ids, rows, dv, tr, K, d, scale, Y, st);
+        default: return lookup_launch<T, V, 32>(C, ids, rows, dv, tr, K, d, scale, Y, st);
     }
 }
 template <typename T>
@@ -401,10 +451,10 @@ km_status lookup_typed(const void *Cv, const int32_t *ids, int64_t B, int64_t N,
         const int Ki = static_cast<int>(K), di = static_cast<int>(d);
         km_status s;
         switch (v * sizeof(T)) {
-            case 16: s = lookup_tpr<T, 16 / sizeof(T)>(Cb, ib, rows, dv, Ki, di, scale, Yb, st); break;
-            case 8: s = lookup_tpr<T, 8 / sizeof(T)>(Cb, ib, rows, dv, Ki, di, scale, Yb, st); break;
-            case 4: s = lookup_tpr<T, 4 / sizeof(T)>(Cb, ib, rows, dv, Ki, di, scale, Yb, st); break;
-            default: s = lookup_tpr<T, 1>(Cb, ib, rows, dv, Ki, di, scale, Yb, st); break;
+            case 16: s = lookup_tpr<T, 16 / sizeof(T)>(Cb, ib, rows, dv, std::min(nb_max, B - b0) * K, Ki, di, scale, Yb, st); break;
+            case 8: s = lookup_tpr<T, 8 / sizeof(T)>(Cb, ib, rows, dv, std::min(nb_max, B - b0) * K, Ki, di, scale, Yb, st); break;
+            case 4: s = lookup_tpr<T, 4 / sizeof(T)>(Cb, ib, rows, dv, std::min(nb_max, B - b0) * K, Ki, di, scale, Yb, st); break;
+            default: s = lookup_tpr<T, 1>(Cb, ib, rows, dv, std::min(nb_max, B - b0) * K, Ki, di, scale, Yb, st); break;
         }
         if (s != KM_OK) return s;
     }
