@@ -106,56 +106,78 @@ __global__ void __launch_bounds__(kLookupThreads)
     }
 }
 
-// ------------------------------------------------------------------ stable radix sort by id
+// ------------------------------------------------------------------ stable sort by id
+//
+// Tokens are sorted by (batch, id), equal ids in token order; ids outside [0, K) are dropped. A
+// least-significant-digit radix sort over the id's bits, digits of up to 11 bits. Where every
+// batch is long, batches are segments that are sorted side by side on the id alone (their order
+// is already that of the keys); where batches are short, all tokens are one segment with keys
+// b K + id. Up to kSmallMax tokens one block sorts everything in shared memory.
+
+struct SortSpec {
+    const int32_t *ids;
+    FastDiv divN;            // batch of a token
+    uint32_t N, K;           // per batch
+    uint32_t n;              // tokens of a segment (at most)
+    uint32_t segs, tps;      // segments, tiles per segment
+    int bins;                // of this pass (a power of two)
+    int shift;
+    int by_batch;            // segments are batches: the digit is taken of the id, not of b K + id
+    const uint32_t *keys, *pos;   // entries of the pass before (first pass: null)
+    const uint32_t *segstart;     // [segs + 1] valid entries of earlier segments (later passes)
+};
 
 constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortItems = 16;
 constexpr int kSortTile = kSortThreads * kSortItems;
-constexpr int kBins = 256;
+constexpr int kMaxBins = 2048;
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallItems = 16;
+constexpr int kSmallMax = kSmallThreads * kSmallItems;
+constexpr int kSmallBins = 512;
 
-struct SortIn {
-    const int32_t *ids;      // first pass: the ids themselves (else null)
-    FastDiv divN;
-    int K;
-    const uint32_t *keys, *pos;   // later passes
-    const uint32_t *nvalid;       // later passes: number of sorted entries
-    uint32_t n;
-};
-
-// Entry i: its key (b K + id) and position; false past the end or for an id outside [0, K).
-__device__ __forceinline__ bool sort_load(const SortIn &s, uint32_t n, uint32_t i, uint32_t &key,
-                                          uint32_t &pos) {
-    if (i >= n) return false;
-    if (s.ids) {
-        const int id = s.ids[i];
-        pos = i;
-        key = fd_div(s.divN, i) * static_cast<uint32_t>(s.K) + static_cast<uint32_t>(id);
-        return id >= 0 && id < s.K;
+// Entry i of segment `seg`: its key (b K + id), token and digit source; false past the segment's
+// end or for an id outside [0, K).
+__device__ __forceinline__ bool sort_load(const SortSpec &s, uint32_t seg, uint32_t i, uint32_t &key, uint32_t &pos) {
+    if (!s.keys) {
+        if (i >= s.n) return false;
+        pos = seg * s.n + i;
+        const uint32_t id = static_cast<uint32_t>(s.ids[pos]);
+        key = fd_div(s.divN, pos) * s.K + id;
+        return id < s.K;
     }
-    key = s.keys[i];
-    pos = s.pos[i];
+    const uint32_t a = s.segstart[seg], e = s.segstart[seg + 1];
+    if (i >= e - a) return false;
+    key = s.keys[a + i];
+    pos = s.pos[a + i];
     return true;
 }
-
-// Digit counts of each tile: counts[bin * tiles + tile].
-__global__ void __launch_bounds__(kSortThreads)
-    sort_hist_kernel(SortIn in, int shift, uint32_t tiles, uint32_t *__restrict__ counts) {
-    __shared__ uint32_t bins[kBins];
-    bins[threadIdx.x] = 0;
-    __syncthreads();
-    const uint32_t n = in.nvalid ? *in.nvalid : in.n;
-    const uint32_t t0 = blockIdx.x * static_cast<uint32_t>(kSortTile);
-    for (int i = 0; i < kSortItems; ++i) {
-        uint32_t key, pos;
-        if (sort_load(in, n, t0 + i * kSortThreads + threadIdx.x, key, pos))
-            atomicAdd(&bins[(key >> shift) & (kBins - 1)], 1u);
-    }
-    __syncthreads();
-    counts[threadIdx.x * static_cast<size_t>(tiles) + blockIdx.x] = bins[threadIdx.x];
+__device__ __forceinline__ uint32_t sort_digit(const SortSpec &s, uint32_t seg, uint32_t key) {
+    return ((s.by_batch ? key - seg * s.K : key) >> s.shift) & (s.bins - 1);
 }
 
-// Inclusive scan over the block; *total receives the sum.
+// Digit counts of each tile: counts[(seg * tps + tile) * bins + bin].
+__global__ void __launch_bounds__(kSortThreads)
+    sort_hist_kernel(const SortSpec s, uint32_t *__restrict__ counts) {
+    __shared__ uint32_t bins[kMaxBins];
+    for (int b = threadIdx.x; b < s.bins; b += kSortThreads) bins[b] = 0;
+    __syncthreads();
+    const uint32_t seg = blockIdx.x / s.tps, tile = blockIdx.x - seg * s.tps;
+    uint32_t key[kSortItems], pos;
+    bool ok[kSortItems];
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i)
+        ok[i] = sort_load(s, seg, tile * kSortTile + i * kSortThreads + threadIdx.x, key[i], pos);
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i)
+        if (ok[i]) atomicAdd(&bins[sort_digit(s, seg, key[i])], 1u);
+    __syncthreads();
+    uint32_t *out = counts + static_cast<size_t>(blockIdx.x) * s.bins;
+    for (int b = threadIdx.x; b < s.bins; b += kSortThreads) out[b] = bins[b];
+}
+
+// Exclusive scan of one value per thread over the block; *total receives the sum.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, uint32_t *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     uint32_t x = v;
@@ -166,215 +188,431 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, 
     }
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    uint32_t before = 0, all = 0;
-    for (int w = 0; w < nw; ++w) {
-        const uint32_t s = warp_sums[w];
-        if (w < warp) before += s;
-        all += s;
+    uint32_t w = lane < nw ? warp_sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
+    const uint32_t before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
+    *total = __shfl_sync(0xffffffffu, w, 31);
     __syncthreads();
-    *total = all;
-    return x + before;
+    return x - v + before;
 }
 
-// One block per bin: exclusive scan of the bin's tile counts in place, its total in totals[bin].
-__global__ void __launch_bounds__(kSortThreads)
-    sort_scan_kernel(uint32_t tiles, uint32_t *__restrict__ counts, uint32_t *__restrict__ totals) {
-    __shared__ uint32_t ws[kSortWarps];
-    uint32_t *c = counts + blockIdx.x * static_cast<size_t>(tiles);
+// Tile counts -> exclusive scan over a segment's tiles, in place, and the totals per (segment,
+// bin); the block that finishes last scans the totals into the start of every (segment, bin) and
+// of every segment. A block covers 32 bins of a segment, its 32 warps a slice of the tiles each.
+__global__ void __launch_bounds__(1024)
+    sort_scan_kernel(const SortSpec s, uint32_t *__restrict__ counts, uint32_t *totals, uint32_t *segstart_out,
+                     unsigned int *done) {
+    __shared__ uint32_t slice[32][33];
+    __shared__ uint32_t ws[32];
+    __shared__ bool last;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const uint32_t bpb = (s.bins + 31) / 32;
+    const uint32_t seg = blockIdx.x / bpb, bin = (blockIdx.x - seg * bpb) * 32 + lane;
+    const bool in = bin < static_cast<uint32_t>(s.bins);
+    uint32_t *c = counts + static_cast<size_t>(seg) * s.tps * s.bins + bin;
+    const uint32_t per = (s.tps + 31) / 32, a = min(s.tps, w * per), e = min(s.tps, a + per);
+    uint32_t sum = 0;
+    if (in)
+        for (uint32_t t = a; t < e; ++t) sum += c[static_cast<size_t>(t) * s.bins];
+    slice[w][lane] = sum;
+    __syncthreads();
     uint32_t run = 0;
-    for (uint32_t t = 0; t < tiles; t += kSortThreads) {
-        const uint32_t i = t + threadIdx.x;
-        const uint32_t v = i < tiles ? c[i] : 0;
-        uint32_t tot;
-        const uint32_t x = block_scan(v, ws, &tot);
-        if (i < tiles) c[i] = run + x - v;
-        run += tot;
+    for (int k = 0; k < w; ++k) run += slice[k][lane];
+    if (in) {
+        for (uint32_t t = a; t < e; ++t) {
+            const uint32_t v = c[static_cast<size_t>(t) * s.bins];
+            c[static_cast<size_t>(t) * s.bins] = run;
+            run += v;
+        }
+        if (w == 31) totals[seg * s.bins + bin] = run;
     }
-    if (threadIdx.x == 0) totals[blockIdx.x] = run;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(done, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    const uint32_t all = s.segs * s.bins;
+    uint32_t base = 0;
+    for (uint32_t i0 = 0; i0 < all; i0 += 4096) {
+        uint32_t v[4], own = 0;
+        const uint32_t i = i0 + threadIdx.x * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] = i + k < all ? __ldcg(totals + i + k) : 0;
+            own += v[k];
+        }
+        uint32_t tot, x = base + block_scan(own, ws, &tot);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < all) {
+                totals[i + k] = x;
+                if ((i + k) % s.bins == 0) segstart_out[(i + k) / s.bins] = x;
+                x += v[k];
+            }
+        base += tot;
+    }
+    if (threadIdx.x == 0) {
+        segstart_out[s.segs] = base;
+        *done = 0;
+    }
 }
 
-// Places every entry of a tile at (bin start) + (entries of the bin in earlier tiles) + (earlier
-// entries of the bin in this tile). Within a warp the rank among equal digits comes from a
-// match over 32 consecutive entries, so the order of equal digits is kept.
+// Places every entry of a tile at (start of its bin) + (entries of the bin in earlier tiles) +
+// (earlier entries of the bin in this tile). Within a warp the rank among equal digits comes from
+// a match over 32 consecutive entries, so the order of equal digits is kept.
 __global__ void __launch_bounds__(kSortThreads)
-    sort_scatter_kernel(SortIn in, int shift, uint32_t tiles, const uint32_t *__restrict__ counts,
-                        const uint32_t *__restrict__ totals, uint32_t *__restrict__ keys_out,
-                        uint32_t *__restrict__ pos_out, uint32_t *__restrict__ nvalid_out) {
-    __shared__ uint32_t ws[kSortWarps];
-    __shared__ uint32_t wcount[kSortWarps][kBins];
-    __shared__ uint32_t base[kBins];
+    sort_scatter_kernel(const SortSpec s, const uint32_t *__restrict__ counts, const uint32_t *__restrict__ starts,
+                        uint32_t *__restrict__ keys_out, uint32_t *__restrict__ pos_out) {
+    extern __shared__ uint32_t dyn[];
+    uint32_t *base = dyn;                                            // [bins]
+    uint16_t *wcount = reinterpret_cast<uint16_t *>(dyn + s.bins);   // [warps][bins]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int w = 0; w < kSortWarps; ++w) wcount[w][threadIdx.x] = 0;
-    uint32_t all;
-    const uint32_t v = totals[threadIdx.x];
-    const uint32_t x = block_scan(v, ws, &all);
-    base[threadIdx.x] = x - v + counts[threadIdx.x * static_cast<size_t>(tiles) + blockIdx.x];
-    if (nvalid_out && blockIdx.x == 0 && threadIdx.x == 0) *nvalid_out = all;
-    __syncthreads();
-    const uint32_t n = in.nvalid ? *in.nvalid : in.n;
-    const uint32_t i0 = blockIdx.x * static_cast<uint32_t>(kSortTile) + warp * (32 * kSortItems) + lane;
-    uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems];
+    const uint32_t seg = blockIdx.x / s.tps, tile = blockIdx.x - seg * s.tps;
+    const uint32_t i0 = tile * kSortTile + warp * (32 * kSortItems) + lane;
+    uint32_t key[kSortItems], pos[kSortItems];
+    uint16_t rank[kSortItems];
     bool ok[kSortItems];
 #pragma unroll
-    for (int i = 0; i < kSortItems; ++i) ok[i] = sort_load(in, n, i0 + i * 32, key[i], pos[i]);
+    for (int i = 0; i < kSortItems; ++i) ok[i] = sort_load(s, seg, i0 + i * 32, key[i], pos[i]);
+    const uint32_t *c = counts + static_cast<size_t>(blockIdx.x) * s.bins;
+    for (int b = threadIdx.x; b < s.bins; b += kSortThreads) {
+        base[b] = starts[seg * s.bins + b] + c[b];
+        for (int w = 0; w < kSortWarps; ++w) wcount[w * s.bins + b] = 0;
+    }
+    __syncthreads();
+    uint16_t *mine = wcount + warp * s.bins;
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
-        const uint32_t digit = ok[i] ? (key[i] >> shift) & (kBins - 1) : kBins;
+        const uint32_t digit = ok[i] ? sort_digit(s, seg, key[i]) : kMaxBins;
         const uint32_t peers = __match_any_sync(0xffffffffu, digit);
         uint32_t prior = 0;
-        if (ok[i]) prior = wcount[warp][digit];
+        if (ok[i]) prior = mine[digit];
         __syncwarp();
-        rank[i] = prior + __popc(peers & ((1u << lane) - 1));
-        if (ok[i] && lane == __ffs(peers) - 1) wcount[warp][digit] = prior + __popc(peers);
+        rank[i] = static_cast<uint16_t>(prior + __popc(peers & ((1u << lane) - 1)));
+        if (ok[i] && lane == __ffs(peers) - 1) mine[digit] = static_cast<uint16_t>(prior + __popc(peers));
         __syncwarp();
     }
     __syncthreads();
-    {
-        uint32_t run = base[threadIdx.x];
+    for (int b = threadIdx.x; b < s.bins; b += kSortThreads) {
+        uint32_t run = 0;
         for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t c = wcount[w][threadIdx.x];
-            wcount[w][threadIdx.x] = run;
-            run += c;
+            const uint32_t v = wcount[w * s.bins + b];
+            wcount[w * s.bins + b] = static_cast<uint16_t>(run);
+            run += v;
         }
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i)
         if (ok[i]) {
-            const uint32_t at = wcount[warp][(key[i] >> shift) & (kBins - 1)] + rank[i];
+            const uint32_t digit = sort_digit(s, seg, key[i]);
+            const uint32_t at = base[digit] + mine[digit] + rank[i];
             keys_out[at] = key[i];
             pos_out[at] = pos[i];
         }
+}
+
+// Zeros over [p, p + bytes), spread over `threads` threads of which this is number i.
+__device__ __forceinline__ void zero_fill(uint8_t *p, size_t bytes, size_t i, size_t threads) {
+    size_t head = (16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15;
+    if (head > bytes) head = bytes;
+    if (i < head) p[i] = 0;
+    uint4 *v = reinterpret_cast<uint4 *>(p + head);
+    const size_t units = (bytes - head) / 16;
+    for (size_t u = i; u < units; u += threads) v[u] = make_uint4(0u, 0u, 0u, 0u);
+    const size_t tail = head + units * 16;
+    if (tail + i < bytes) p[tail + i] = 0;
+}
+
+// Up to kSmallMax tokens: block 0 sorts them in shared memory (digits of at most 9 bits; dropped
+// tokens carry the key B K and end up behind the others) while the other blocks zero the table's
+// gradient, which for a large table takes longer than the sort.
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    sort_small_kernel(const SortSpec s, uint32_t tokens, uint32_t keys_total, int passes, int width,
+                      uint32_t *__restrict__ keys_out, uint32_t *__restrict__ pos_out, uint32_t *__restrict__ nvalid,
+                      unsigned int *__restrict__ jobs, uint8_t *zero, size_t zero_bytes) {
+    if (blockIdx.x > 0) {
+        if (zero)
+            zero_fill(zero, zero_bytes, static_cast<size_t>(blockIdx.x - 1) * kSmallThreads + threadIdx.x,
+                      static_cast<size_t>(gridDim.x - 1) * kSmallThreads);
+        return;
+    }
+    extern __shared__ uint32_t dyn[];
+    __shared__ uint32_t ws[32];
+    uint32_t *skeys = dyn;                                                   // [kSmallMax]
+    uint16_t *spos = reinterpret_cast<uint16_t *>(dyn + kSmallMax);          // [kSmallMax]
+    uint16_t *wcount = spos + kSmallMax;                                     // [32][kSmallBins]
+    uint32_t *base = reinterpret_cast<uint32_t *>(wcount + 32 * kSmallBins);  // [kSmallBins]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = static_cast<int>((tokens + kSmallThreads - 1) / kSmallThreads);
+    const uint32_t i0 = static_cast<uint32_t>(warp * 32 * per + lane);
+    uint32_t key[kSmallItems];
+    uint16_t pos[kSmallItems], rank[kSmallItems];
+    int valid = 0;
+#pragma unroll
+    for (int i = 0; i < kSmallItems; ++i)
+        if (i < per) {
+            const uint32_t at = i0 + i * 32;
+            pos[i] = static_cast<uint16_t>(at);
+            key[i] = 0xffffffffu;                 // no entry at all
+            if (at < tokens) {
+                const uint32_t id = static_cast<uint32_t>(s.ids[at]);
+                key[i] = id < s.K ? fd_div(s.divN, at) * s.K + id : keys_total;
+                valid += id < s.K;
+            }
+        }
+    {
+        uint32_t tot;
+        block_scan(static_cast<uint32_t>(valid), ws, &tot);
+        if (threadIdx.x == 0) {
+            *nvalid = tot;
+            *jobs = 0;
+        }
+    }
+    const int bins = 1 << width;
+    uint16_t *mine = wcount + warp * kSmallBins;
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = pass * width;
+        for (int b = threadIdx.x; b < 32 * kSmallBins / 2; b += kSmallThreads) reinterpret_cast<uint32_t *>(wcount)[b] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSmallItems; ++i)
+            if (i < per) {
+                const bool ok = i0 + i * 32 < tokens;
+                const uint32_t digit = ok ? (key[i] >> shift) & (bins - 1) : kSmallBins;
+                const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+                uint32_t prior = 0;
+                if (ok) prior = mine[digit];
+                __syncwarp();
+                rank[i] = static_cast<uint16_t>(prior + __popc(peers & ((1u << lane) - 1)));
+                if (ok && lane == __ffs(peers) - 1) mine[digit] = static_cast<uint16_t>(prior + __popc(peers));
+                __syncwarp();
+            }
+        __syncthreads();
+        uint32_t sum = 0;
+        if (threadIdx.x < bins)
+            for (int w = 0; w < 32; ++w) {
+                const uint32_t v = wcount[w * kSmallBins + threadIdx.x];
+                wcount[w * kSmallBins + threadIdx.x] = static_cast<uint16_t>(sum);
+                sum += v;
+            }
+        uint32_t tot;
+        const uint32_t start = block_scan(sum, ws, &tot);
+        if (threadIdx.x < bins) base[threadIdx.x] = start;
+        __syncthreads();
+        const bool final = pass + 1 == passes;
+#pragma unroll
+        for (int i = 0; i < kSmallItems; ++i)
+            if (i < per && i0 + i * 32 < tokens) {
+                const uint32_t digit = (key[i] >> shift) & (bins - 1);
+                const uint32_t at = base[digit] + mine[digit] + rank[i];
+                if (final) {
+                    keys_out[at] = key[i];
+                    pos_out[at] = pos[i];
+                } else {
+                    skeys[at] = key[i];
+                    spos[at] = pos[i];
+                }
+            }
+        if (final) break;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSmallItems; ++i)
+            if (i < per && i0 + i * 32 < tokens) {
+                key[i] = skeys[i0 + i * 32];
+                pos[i] = spos[i0 + i * 32];
+            }
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------------ sums over the sorted order
 
 struct GradParams {
     const uint32_t *keys, *pos, *nvalid;
-    uint32_t range;   // sorted entries per range
-    int d;
+    uint32_t range;        // sorted entries per range, before its ends move to the ends of runs
+    uint32_t units;        // per row
     float scale;
     int accumulate;
-    float *slots;     // [ranges][2][d] fp32: the range's first and last run where they go on
-                      // in a neighbouring range
+    float *slots;          // [ranges][2][d] fp32: the range's first and last run where they are cut
+    uint32_t *jobs;        // [0] count, then the first range of every cut run
 };
 
 template <typename O, int V>
 __device__ __forceinline__ void write_row(O *out, const float (&acc)[V], float scale, int accumulate) {
-    Vec<O, V> o;
-    if (accumulate) o = *reinterpret_cast<const Vec<O, V> *>(out);
+    constexpr int VO = 16 / sizeof(O) < V ? 16 / sizeof(O) : V;      // at most 16 bytes per access
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float s = scale * acc[i];
-        o.v[i] = Cvt<O>::from_f(accumulate ? Cvt<O>::to_f(o.v[i]) + s : s);
+    for (int h = 0; h < V; h += VO) {
+        Vec<O, VO> o;
+        if (accumulate) o = *reinterpret_cast<const Vec<O, VO> *>(out + h);
+#pragma unroll
+        for (int i = 0; i < VO; ++i) {
+            const float s = scale * acc[h + i];
+            o.v[i] = Cvt<O>::from_f(accumulate ? Cvt<O>::to_f(o.v[i]) + s : s);
+        }
+        *reinterpret_cast<Vec<O, VO> *>(out + h) = o;
     }
-    *reinterpret_cast<Vec<O, V> *>(out) = o;
 }
 
 constexpr int kGradThreads = 256;
 
-// LPR lanes per range and column block of LPR * V columns. A range adds up the rows of its runs
-// of equal keys one after the other in fp32; a run that begins and ends inside the range is
-// written to its table row, the others to the range's slots.
+// Where range r begins: the first start of a run in [r L, (r + 1) L), so that a run is summed by
+// one range; a run that covers all of it is cut at r L. The LPR lanes of a group search together;
+// every lane of the warp takes part.
+template <int LPR>
+__device__ __forceinline__ uint32_t range_begin(const uint32_t *keys, uint32_t n, uint64_t at, uint32_t L, bool &cut) {
+    const int t = threadIdx.x % LPR;
+    const uint32_t gmask = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1) << ((threadIdx.x & 31) / LPR * LPR);
+    cut = false;
+    const bool inside = at < n && at > 0;
+    uint32_t found = at >= n ? n : static_cast<uint32_t>(at);
+    bool open = inside;
+    for (uint32_t o = 0; o < L; o += LPR) {
+        if (!__any_sync(0xffffffffu, open)) break;
+        const uint64_t i = at + o + t;
+        bool start = false;
+        if (open && o + t < L) start = i >= n || keys[i] != keys[i - 1];
+        const uint32_t b = __ballot_sync(0xffffffffu, start) & gmask;
+        if (open && b) {
+            const uint64_t f = at + o + (__ffs(b) - 1) % LPR;
+            found = f < n ? static_cast<uint32_t>(f) : n;
+            open = false;
+        }
+    }
+    cut = open;
+    return found;
+}
+
+// LPR lanes per range and V columns per lane. A range adds up the rows of its runs of equal keys
+// one after the other in fp32; a whole run goes to its table row, a cut one to the range's slots,
+// and the range that a cut run begins in enters the run into the list of joins.
 template <typename T, typename O, int V, int LPR>
 __global__ void __launch_bounds__(kGradThreads)
-    grad_ranges_kernel(const T *__restrict__ dY, GradParams p, O *__restrict__ dC) {
+    grad_ranges_kernel(const T *__restrict__ dY, const GradParams p, O *__restrict__ dC) {
     constexpr int GROUPS = kGradThreads / LPR;
-    constexpr int U = 8;   // rows in flight per group
-    const int g = threadIdx.x / LPR, t = threadIdx.x % LPR;
+    constexpr int U = LPR < 8 ? LPR : (V * sizeof(T) >= 16 ? 4 : 8);   // rows in flight per group
+    const int t = threadIdx.x % LPR;
     const uint32_t n = *p.nvalid;
-    const uint32_t r = blockIdx.x * static_cast<uint32_t>(GROUPS) + g;
-    const uint64_t s64 = static_cast<uint64_t>(r) * p.range;
-    if (s64 >= n) return;
-    const uint32_t s = static_cast<uint32_t>(s64);
-    const uint32_t e = static_cast<uint32_t>(min(static_cast<uint64_t>(n), s64 + p.range));
-    const int c = (blockIdx.y * LPR + t) * V;
-    if (c >= p.d) return;
+    const uint32_t r = blockIdx.x * static_cast<uint32_t>(GROUPS) + threadIdx.x / LPR;
+    const uint64_t first = static_cast<uint64_t>(r) * p.range;
+    bool cut0, cut1;
+    const uint32_t s = range_begin<LPR>(p.keys, n, first, p.range, cut0);
+    const uint32_t e = range_begin<LPR>(p.keys, n, first + p.range, p.range, cut1);
+    const uint32_t len = e - s;                     // at most two ranges' entries
+    const uint32_t c = blockIdx.y * LPR + t;
+    const bool in = c < p.units;
+    const int64_t d = static_cast<int64_t>(p.units) * V;
+    const Vec<T, V> *src = reinterpret_cast<const Vec<T, V> *>(dY);
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    uint32_t cur = p.keys[s];
-    bool head = s > 0 && p.keys[s - 1] == cur;
+    bool head = cut0;
+    uint32_t cur = 0;
     auto flush = [&](bool tail) {
+        if (!in) return;
         if (head || tail) {
-            float *slot = p.slots + (static_cast<size_t>(r) * 2 + (head ? 0 : 1)) * p.d + c;
+            float *slot = p.slots + (static_cast<int64_t>(r) * 2 + (head ? 0 : 1)) * d + static_cast<int64_t>(c) * V;
 #pragma unroll
             for (int i = 0; i < V; ++i) slot[i] = acc[i];
         } else {
-            write_row<O, V>(dC + static_cast<int64_t>(cur) * p.d + c, acc, p.scale, p.accumulate);
+            write_row<O, V>(dC + static_cast<int64_t>(cur) * d + static_cast<int64_t>(c) * V, acc, p.scale, p.accumulate);
         }
     };
-    for (uint32_t i = s; i < e; i += U) {
-        uint32_t key[U];
-        Vec<T, V> v[U];
+    for (uint32_t b = 0; __any_sync(0xffffffffu, b < len); b += LPR) {
+        const bool have = b + t < len;
+        const uint32_t key = have ? p.keys[s + b + t] : 0, pos = have ? p.pos[s + b + t] : 0;
+        if (b == 0) cur = __shfl_sync(0xffffffffu, key, 0, LPR);
+#pragma unroll 1
+        for (int u0 = 0; u0 < LPR; u0 += U) {
+            if (!__any_sync(0xffffffffu, b + u0 < len)) break;
+            Vec<T, V> v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i + u < e) {
-                key[u] = p.keys[i + u];
-                v[u] = *reinterpret_cast<const Vec<T, V> *>(dY + static_cast<int64_t>(p.pos[i + u]) * p.d + c);
+            for (int u = 0; u < U; ++u) {
+                const uint32_t row = __shfl_sync(0xffffffffu, pos, u0 + u, LPR);
+                if (b + u0 + u < len && in) v[u] = load_ro(src + static_cast<int64_t>(row) * p.units + c);
             }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i + u < e) {
-                if (key[u] != cur) {
-                    flush(false);
-                    cur = key[u];
-                    head = false;
+            for (int u = 0; u < U; ++u) {
+                const uint32_t k = __shfl_sync(0xffffffffu, key, u0 + u, LPR);
+                if (b + u0 + u < len) {
+                    if (k != cur) {
+                        flush(false);
+                        cur = k;
+                        head = false;
 #pragma unroll
-                    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+                        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+                    }
+                    if (in)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) acc[i] += Cvt<T>::to_f(v[u].v[i]);
                 }
-#pragma unroll
-                for (int k = 0; k < V; ++k) acc[k] += Cvt<T>::to_f(v[u].v[k]);
             }
+        }
     }
-    flush(e < n && p.keys[e] == cur);
+    if (len) {
+        if (cut1 && !head && t == 0 && blockIdx.y == 0) p.jobs[1 + atomicAdd(p.jobs, 1u)] = r;
+        flush(cut1);
+    }
 }
 
-// One block per range: joins, in range order, the pieces of the run that begins in this range
-// and goes on in the next ones.
-template <typename O, int V, int LPR>
+// Joins the pieces of the cut runs, each in range order: a block per run and 32 V columns takes the
+// runs off the list (whose order does not matter: every run is a row of its own); its eight warps
+// add up consecutive pieces, then the eight sums in order.
+template <typename O, int V>
 __global__ void __launch_bounds__(kGradThreads)
-    grad_join_kernel(GradParams p, O *__restrict__ dC) {
-    constexpr int GROUPS = kGradThreads / LPR;
-    __shared__ float part[GROUPS][LPR * V];
-    const uint32_t n = *p.nvalid;
-    const uint64_t s64 = static_cast<uint64_t>(blockIdx.x) * p.range;
-    if (s64 + p.range >= n) return;                       // nothing follows this range
-    const uint32_t s = static_cast<uint32_t>(s64), e = s + p.range;
-    const uint32_t key = p.keys[e - 1];
-    if (p.keys[e] != key) return;                         // its last run ends with it
-    if (p.keys[s] == key && s > 0 && p.keys[s - 1] == key) return;   // the run began earlier
-    uint32_t lo = e, hi = n;                              // first entry behind the run
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (p.keys[mid] == key) lo = mid + 1; else hi = mid;
-    }
-    const uint32_t r0 = blockIdx.x, r1 = (lo - 1) / p.range;   // first and last range of the run
-    const uint32_t len = r1 - r0 + 1, per = (len + GROUPS - 1) / GROUPS;
-    const int g = threadIdx.x / LPR, t = threadIdx.x % LPR;
-    for (int c0 = 0; c0 < p.d; c0 += LPR * V) {
-        const int c = c0 + t * V;
+    grad_join_kernel(const GradParams p, O *__restrict__ dC) {
+    constexpr int WARPS = kGradThreads / 32;
+    __shared__ float part[WARPS][32 * V];
+    const uint32_t n = *p.nvalid, njobs = p.jobs[0];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t d = static_cast<int64_t>(p.units) * V;
+    const uint32_t c = blockIdx.y * 32 + lane;
+    const bool in = c < p.units;
+    for (uint32_t job = blockIdx.x; job < njobs; job += gridDim.x) {
+        const uint32_t r0 = p.jobs[1 + job];
+        const uint32_t cut = (r0 + 1) * p.range;            // an entry of the run, the first behind r0
+        const uint32_t key = p.keys[cut];
+        // the run's end, 32 probes at a time
+        uint32_t lo = cut, hi = n;                           // keys[lo] == key; hi is behind the run
+        while (hi - lo > 1) {
+            const uint32_t step = (hi - lo + 31) / 32;
+            const uint64_t at = static_cast<uint64_t>(lo) + static_cast<uint64_t>(lane) * step;
+            const bool same = at < hi && p.keys[at] == key;
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, same));
+            const uint64_t nhi = static_cast<uint64_t>(lo) + static_cast<uint64_t>(k + 1) * step;
+            lo += k * step;
+            if (nhi < hi) hi = static_cast<uint32_t>(nhi);
+        }
+        // The last piece: the run ends at lo; it was cut at every multiple of the range whose whole
+        // range it covers, i.e. up to the last r with r L + L <= lo + 1.
+        const uint32_t r1 = (lo + 1) / p.range - 1;
+        const uint32_t count = r1 - r0 + 1, per = (count + WARPS - 1) / WARPS;
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        if (c < p.d) {
-            const uint32_t a = min(len, g * per), b = min(len, a + per);
+        if (in) {
+            const uint32_t a = min(count, w * per), e = min(count, a + per);
+            const float *slot = p.slots + static_cast<int64_t>(c) * V;
 #pragma unroll 4
-            for (uint32_t j = a; j < b; ++j) {
-                const float *slot = p.slots + (static_cast<size_t>(r0 + j) * 2 + (j == 0 ? 1 : 0)) * p.d + c;
+            for (uint32_t j = a; j < e; ++j) {
+                const float *q = slot + (static_cast<int64_t>(r0 + j) * 2 + (j == 0 ? 1 : 0)) * d;
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += slot[i];
+                for (int i = 0; i < V; ++i) acc[i] += q[i];
             }
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) part[g][t * V + i] = acc[i];
+        for (int i = 0; i < V; ++i) part[w][i * 32 + lane] = acc[i];
         __syncthreads();
-        if (g == 0 && c < p.d) {
-            for (int q = 1; q < GROUPS; ++q)
+        if (w == 0 && in) {
+            for (int q = 1; q < WARPS; ++q)
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += part[q][t * V + i];
-            write_row<O, V>(dC + static_cast<int64_t>(key) * p.d + c, acc, p.scale, p.accumulate);
+                for (int i = 0; i < V; ++i) acc[i] += part[q][i * 32 + lane];
+            write_row<O, V>(dC + static_cast<int64_t>(key) * d + static_cast<int64_t>(c) * V, acc, p.scale, p.accumulate);
         }
         __syncthreads();
     }
@@ -463,43 +701,149 @@ km_status lookup_typed(const void *Cv, const int32_t *ids, int64_t B, int64_t N,
 
 // ------------------------------------------------------------------ gradient
 
+// How the tokens of a call are sorted.
+struct SortPlan {
+    bool small;              // one block, in shared memory
+    int64_t segs, n, tps;    // otherwise: segments, their tokens, tiles per segment
+    bool by_batch;
+    int passes, width;       // digits
+};
+inline int bits_of(int64_t values) {     // bits that hold 0 .. values - 1
+    int b = 1;
+    while ((int64_t{1} << b) < values) ++b;
+    return b;
+}
+inline SortPlan sort_plan(int64_t B, int64_t N, int64_t K) {
+    SortPlan p = {};
+    p.small = B * N <= kSmallMax;
+    if (p.small) {
+        const int bits = bits_of(B * K + 1);
+        p.passes = static_cast<int>(ceil_div(bits, 9));
+        p.width = static_cast<int>(ceil_div(bits, p.passes));
+        return p;
+    }
+    // Batches of at least half a tile are segments (their sort needs the bits of the id alone), as
+    // long as one block can scan the starts of all their bins.
+    int bits = bits_of(K);
+    p.passes = static_cast<int>(ceil_div(bits, 11));
+    p.width = static_cast<int>(ceil_div(bits, p.passes));
+    p.by_batch = N >= kSortTile / 2 && (B << p.width) <= 65536;
+    if (!p.by_batch) {
+        bits = bits_of(B * K);
+        p.passes = static_cast<int>(ceil_div(bits, 11));
+        p.width = static_cast<int>(ceil_div(bits, p.passes));
+    }
+    p.segs = p.by_batch ? B : 1;
+    p.n = p.by_batch ? N : B * N;
+    p.tps = ceil_div(p.n, kSortTile);
+    return p;
+}
+
+// Entries per range: as many ranges as fill the device with their groups (32 per SM on 148 SMs), at
+// least 16 entries each.
+inline int64_t grad_range(int64_t T) { return std::max<int64_t>(16, ceil_div(T, 148 * 64)); }
+
 struct GradWs {
-    uint32_t *keys[2], *pos[2], *counts, *totals, *nvalid;
+    uint32_t *keys[2], *pos[2], *counts, *totals, *segstart, *jobs;
+    unsigned int *done;
     float *slots;
 };
-// Entries per range: enough ranges to fill the device (32 groups per SM on 148 SMs), never
-// shorter than 16 entries.
-inline int64_t grad_range(int64_t T) { return std::max<int64_t>(16, ceil_div(T, 148 * 32)); }
-inline GradWs carve_grad(Carver &c, int64_t T, int64_t d) {
-    GradWs g;
-    const int64_t tiles = ceil_div(T, kSortTile);
-    for (int i = 0; i < 2; ++i) {
+inline GradWs carve_grad(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d) {
+    GradWs g = {};
+    const int64_t T = B * N, ranges = ceil_div(T, grad_range(T));
+    const SortPlan p = sort_plan(B, N, K);
+    for (int i = 0; i < (p.passes > 1 && !p.small ? 2 : 1); ++i) {
         g.keys[i] = c.take<uint32_t>(static_cast<size_t>(T) * 4);
         g.pos[i] = c.take<uint32_t>(static_cast<size_t>(T) * 4);
     }
-    g.counts = c.take<uint32_t>(static_cast<size_t>(kBins * tiles) * 4);
-    g.totals = c.take<uint32_t>(kBins * 4);
-    g.nvalid = c.take<uint32_t>(4);
-    g.slots = c.take<float>(static_cast<size_t>(ceil_div(T, grad_range(T)) * 2 * d) * 4);
+    if (!p.small) {
+        g.counts = c.take<uint32_t>(static_cast<size_t>(p.segs * p.tps << p.width) * 4);
+        g.totals = c.take<uint32_t>(static_cast<size_t>(p.segs << p.width) * 4);
+    }
+    g.segstart = c.take<uint32_t>(static_cast<size_t>(std::max<int64_t>(p.segs, 0) + 1) * 4);
+    g.done = c.take<unsigned int>(4);
+    g.jobs = c.take<uint32_t>(static_cast<size_t>(ranges + 1) * 4);
+    g.slots = c.take<float>(static_cast<size_t>(ranges * 2 * d) * 4);
     return g;
 }
 inline bool grad_sizes_ok(int64_t B, int64_t N, int64_t K, int64_t d) {
-    return sizes_ok(B, N, K, d) && B * N <= kMaxIndex && B * K <= kMaxIndex;
+    return sizes_ok(B, N, K, d) && B * N <= kMaxIndex && B * K < kMaxIndex;
+}
+
+// Sorts the tokens; *side is the buffer that holds them, *nvalid their number on the device. `zero`
+// (or null) is set to zeros.
+km_status grad_sort(const int32_t *ids, int64_t B, int64_t N, int64_t K, const GradWs &w, void *zero, size_t zero_bytes,
+                    int *side, const uint32_t **nvalid, cudaStream_t st) {
+    const SortPlan p = sort_plan(B, N, K);
+    const int64_t T = B * N;
+    SortSpec s = {};
+    s.ids = ids;
+    s.divN = make_fastdiv(static_cast<uint32_t>(N));
+    s.N = static_cast<uint32_t>(N);
+    s.K = static_cast<uint32_t>(K);
+    if (p.small) {
+        constexpr int kSmem = kSmallMax * 6 + 32 * kSmallBins * 2 + kSmallBins * 4;
+        if (cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+            return KM_ERR_CUDA;
+        // a zeroing block per 64 KB, one per SM at most
+        const int64_t fill = zero ? std::min<int64_t>(num_sms() - 1, ceil_div(static_cast<int64_t>(zero_bytes), 65536)) : 0;
+        sort_small_kernel<<<static_cast<unsigned>(1 + fill), kSmallThreads, kSmem, st>>>(
+            s, static_cast<uint32_t>(T), static_cast<uint32_t>(B * K), p.passes, p.width, w.keys[0], w.pos[0], w.segstart,
+            w.jobs, static_cast<uint8_t *>(zero), zero_bytes);
+        *side = 0;
+        *nvalid = w.segstart;
+        return launch_status();
+    }
+    if ((zero && cudaMemsetAsync(zero, 0, zero_bytes, st) != cudaSuccess) ||
+        cudaMemsetAsync(w.done, 0, 4, st) != cudaSuccess || cudaMemsetAsync(w.jobs, 0, 4, st) != cudaSuccess ||
+        cudaFuncSetAttribute(sort_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxBins * (4 + 2 * kSortWarps)) != cudaSuccess)
+        return KM_ERR_CUDA;
+    s.n = static_cast<uint32_t>(p.n);
+    s.segs = static_cast<uint32_t>(p.segs);
+    s.tps = static_cast<uint32_t>(p.tps);
+    s.bins = 1 << p.width;
+    s.by_batch = p.by_batch ? 1 : 0;
+    const int64_t blocks = p.segs * p.tps, sblocks = p.segs * ceil_div(s.bins, 32);
+    if (blocks > kMaxIndex || sblocks > kMaxIndex) return KM_ERR_UNSUPPORTED;
+    *side = 0;
+    for (int pass = 0; pass < p.passes; ++pass) {
+        s.shift = pass * p.width;
+        if (pass) {
+            s.keys = w.keys[*side];
+            s.pos = w.pos[*side];
+            s.segstart = w.segstart;
+            *side ^= 1;
+        }
+        sort_hist_kernel<<<static_cast<unsigned>(blocks), kSortThreads, 0, st>>>(s, w.counts);
+        if (launch_status() != KM_OK) return KM_ERR_CUDA;
+        sort_scan_kernel<<<static_cast<unsigned>(sblocks), 1024, 0, st>>>(s, w.counts, w.totals, w.segstart, w.done);
+        if (launch_status() != KM_OK) return KM_ERR_CUDA;
+        sort_scatter_kernel<<<static_cast<unsigned>(blocks), kSortThreads, s.bins * (4 + 2 * kSortWarps), st>>>(
+            s, w.counts, w.totals, w.keys[*side], w.pos[*side]);
+        if (launch_status() != KM_OK) return KM_ERR_CUDA;
+    }
+    *nvalid = w.segstart + p.segs;
+    return KM_OK;
 }
 
 template <typename T, typename O, int V, int LPR>
 km_status grad_sum(const T *dY, const GradParams &p, int64_t ranges, O *dC, cudaStream_t st) {
-    constexpr int GROUPS = kGradThreads / LPR;
-    dim3 grid(static_cast<unsigned>(ceil_div(ranges, GROUPS)), static_cast<unsigned>(ceil_div(p.d, LPR * V)));
+    const dim3 grid(static_cast<unsigned>(ceil_div(ranges, kGradThreads / LPR)), static_cast<unsigned>(ceil_div(p.units, LPR)));
     if (grid.y > kMaxGridY) return KM_ERR_UNSUPPORTED;   // never: d <= 2^20 and 32 lanes per block
     grad_ranges_kernel<T, O, V, LPR><<<grid, kGradThreads, 0, st>>>(dY, p, dC);
     if (launch_status() != KM_OK) return KM_ERR_CUDA;
-    if (ranges > 1) grad_join_kernel<O, V, LPR><<<static_cast<unsigned>(ranges), kGradThreads, 0, st>>>(p, dC);
+    if (ranges > 1) {
+        const unsigned cols = static_cast<unsigned>(ceil_div(p.units, 32));
+        const unsigned rows = static_cast<unsigned>(std::min<int64_t>(ranges, std::max<int64_t>(1, 148 * 4 / cols)));
+        grad_join_kernel<O, V><<<dim3(rows, cols), kGradThreads, 0, st>>>(p, dC);
+    }
     return launch_status();
 }
 template <typename T, typename O, int V>
-km_status grad_lpr(const T *dY, const GradParams &p, int64_t ranges, O *dC, cudaStream_t st) {
-    switch (pow2_at_least(ceil_div(p.d, V), 32)) {
+km_status grad_lpr(const T *dY, GradParams p, int64_t d, int64_t ranges, O *dC, cudaStream_t st) {
+    p.units = static_cast<uint32_t>(d / V);
+    switch (pow2_at_least(p.units, 32)) {
         case 1: return grad_sum<T, O, V, 1>(dY, p, ranges, dC, st);
         case 2:
         case 4: return grad_sum<T, O, V, 4>(dY, p, ranges, dC, st);
@@ -509,14 +853,17 @@ km_status grad_lpr(const T *dY, const GradParams &p, int64_t ranges, O *dC, cuda
     }
 }
 template <typename T, typename O>
-km_status grad_typed(const void *dYv, const GradParams &p, int64_t ranges, void *dCv, cudaStream_t st) {
+km_status grad_typed(const void *dYv, const GradParams &p, int64_t d, int64_t ranges, void *dCv, cudaStream_t st) {
     const T *dY = static_cast<const T *>(dYv);
     O *dC = static_cast<O *>(dCv);
-    // 8 bytes a lane for 16-bit rows and 16 for fp32: four columns, one vector access on either side
-    const int v = std::min(vec_elems(p.d, sizeof(T), dY, dY), vec_elems(p.d, sizeof(O), dC, dC));
-    if (v >= 4) return grad_lpr<T, O, 4>(dY, p, ranges, dC, st);
-    if (v >= 2) return grad_lpr<T, O, 2>(dY, p, ranges, dC, st);
-    return grad_lpr<T, O, 1>(dY, p, ranges, dC, st);
+    // the widest access that both sides' rows allow: 16 bytes of dY, and whole 16-byte pieces of dC
+    const int vt = vec_elems(d, sizeof(T), dY, dY), vo = vec_elems(d, sizeof(O), dC, dC);
+    const int v = vo * sizeof(O) >= 16 ? vt : std::min(vt, vo);
+    if constexpr (sizeof(T) == 2)
+        if (v >= 8) return grad_lpr<T, O, 8>(dY, p, d, ranges, dC, st);
+    if (v >= 4) return grad_lpr<T, O, 4>(dY, p, d, ranges, dC, st);
+    if (v >= 2) return grad_lpr<T, O, 2>(dY, p, d, ranges, dC, st);
+    return grad_lpr<T, O, 1>(dY, p, d, ranges, dC, st);
 }
 
 }  // namespace
@@ -538,7 +885,7 @@ km_status km_lookup(const void *C, km_dtype dtype, const int32_t *ids, int64_t B
 size_t km_lookup_grad_workspace_size(int64_t B, int64_t N, int64_t K, int64_t d) {
     if (!grad_sizes_ok(B, N, K, d)) return 0;
     Carver c(nullptr);
-    carve_grad(c, B * N, d);
+    carve_grad(c, B, N, K, d);
     return c.off;
 }
 
@@ -552,53 +899,27 @@ km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int
     if (out_dtype != KM_F32 && out_dtype != dtype) return KM_ERR_UNSUPPORTED;
     if (!ws || ws_bytes < km_lookup_grad_workspace_size(B, N, K, d)) return KM_ERR_WORKSPACE;
     cudaStream_t st = S(stream);
-    const int64_t T = B * N;
     Carver c(ws);
-    const GradWs w = carve_grad(c, T, d);
-    if (!accumulate &&
-        cudaMemsetAsync(dC, 0, static_cast<size_t>(B * K * d) * dtype_size(out_dtype), st) != cudaSuccess)
-        return KM_ERR_CUDA;
-    const uint32_t tiles = static_cast<uint32_t>(ceil_div(T, kSortTile));
-    int bits = 1;
-    while ((int64_t{1} << bits) < B * K) ++bits;
-    int side = 0;
-    for (int shift = 0; shift < bits; shift += 8) {
-        SortIn in = {};
-        in.n = static_cast<uint32_t>(T);
-        in.K = static_cast<int>(K);
-        in.divN = make_fastdiv(static_cast<uint32_t>(N));
-        if (shift == 0) {
-            in.ids = ids;
-        } else {
-            in.keys = w.keys[side ^ 1];
-            in.pos = w.pos[side ^ 1];
-            in.nvalid = w.nvalid;
-        }
-        sort_hist_kernel<<<tiles, kSortThreads, 0, st>>>(in, shift, tiles, w.counts);
-        if (launch_status() != KM_OK) return KM_ERR_CUDA;
-        sort_scan_kernel<<<kBins, kSortThreads, 0, st>>>(tiles, w.counts, w.totals);
-        if (launch_status() != KM_OK) return KM_ERR_CUDA;
-        sort_scatter_kernel<<<tiles, kSortThreads, 0, st>>>(in, shift, tiles, w.counts, w.totals, w.keys[side],
-                                                            w.pos[side], shift == 0 ? w.nvalid : nullptr);
-        if (launch_status() != KM_OK) return KM_ERR_CUDA;
-        side ^= 1;
-    }
+    const GradWs w = carve_grad(c, B, N, K, d);
     GradParams p = {};
-    p.keys = w.keys[side ^ 1];
-    p.pos = w.pos[side ^ 1];
-    p.nvalid = w.nvalid;
-    p.range = static_cast<uint32_t>(grad_range(T));
-    p.d = static_cast<int>(d);
+    int side = 0;
+    const km_status s = grad_sort(ids, B, N, K, w, accumulate ? nullptr : dC,
+                                  static_cast<size_t>(B * K * d) * dtype_size(out_dtype), &side, &p.nvalid, st);
+    if (s != KM_OK) return s;
+    p.keys = w.keys[side];
+    p.pos = w.pos[side];
+    p.range = static_cast<uint32_t>(grad_range(B * N));
     p.scale = scale;
     p.accumulate = accumulate ? 1 : 0;
     p.slots = w.slots;
-    const int64_t ranges = ceil_div(T, p.range);
-    if (dtype == KM_F32) return grad_typed<float, float>(dY, p, ranges, dC, st);
+    p.jobs = w.jobs;
+    const int64_t ranges = ceil_div(B * N, p.range);
+    if (dtype == KM_F32) return grad_typed<float, float>(dY, p, d, ranges, dC, st);
     if (dtype == KM_F16)
-        return out_dtype == KM_F32 ? grad_typed<__half, float>(dY, p, ranges, dC, st)
-                                   : grad_typed<__half, __half>(dY, p, ranges, dC, st);
-    return out_dtype == KM_F32 ? grad_typed<__nv_bfloat16, float>(dY, p, ranges, dC, st)
-                               : grad_typed<__nv_bfloat16, __nv_bfloat16>(dY, p, ranges, dC, st);
+        return out_dtype == KM_F32 ? grad_typed<__half, float>(dY, p, d, ranges, dC, st)
+                                   : grad_typed<__half, __half>(dY, p, d, ranges, dC, st);
+    return out_dtype == KM_F32 ? grad_typed<__nv_bfloat16, float>(dY, p, d, ranges, dC, st)
+                               : grad_typed<__nv_bfloat16, __nv_bfloat16>(dY, p, d, ranges, dC, st);
 }
 
 }  // extern "C"
