@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kLookupThreads)
 // ------------------------------------------------------------------ stable sort by id
 //
 // Tokens are sorted by (batch, id), equal ids in token order; ids outside [0, K) are dropped. A
-// least-significant-digit radix sort over the id's bits, digits of up to 11 bits. Where every
+// least-significant-digit radix sort over the id's bits, digits of up to 10 bits. Where every
 // batch is long, batches are segments that are sorted side by side on the id alone (their order
 // is already that of the keys); where batches are short, all tokens are one segment with keys
 // b K + id. Up to kSmallMax tokens one block sorts everything in shared memory.
@@ -117,28 +117,29 @@ __global__ void __launch_bounds__(kLookupThreads)
 struct SortSpec {
     const int32_t *ids;
     FastDiv divN;            // batch of a token
-    uint32_t N, K;           // per batch
+    uint32_t K;              // per batch
     uint32_t n;              // tokens of a segment (at most)
     uint32_t segs, tps;      // segments, tiles per segment
-    int bins;                // of this pass (a power of two)
-    int shift;
+    int width, shift;        // digit of this pass
     int by_batch;            // segments are batches: the digit is taken of the id, not of b K + id
+    int scanned;             // counts hold scans over the tiles, totals the bins' sums
     const uint32_t *keys, *pos;   // entries of the pass before (first pass: null)
-    const uint32_t *segstart;     // [segs + 1] valid entries of earlier segments (later passes)
+    uint32_t *segtotal;      // [segs] valid tokens
+    uint32_t *segstart;      // [segs + 1] their exclusive sums (written by the first scatter)
 };
 
-constexpr int kSortThreads = 256;
+constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortItems = 16;
 constexpr int kSortTile = kSortThreads * kSortItems;
-constexpr int kMaxBins = 2048;
-constexpr int kSmallThreads = 1024;
-constexpr int kSmallItems = 16;
-constexpr int kSmallMax = kSmallThreads * kSmallItems;
-constexpr int kSmallBins = 512;
+constexpr int kMaxWidth = 10;                  // bits of a digit
+constexpr int kMaxBins = 1 << kMaxWidth;
+constexpr int kScanTiles = 64;                 // above this many tiles a kernel of its own scans them
+constexpr int kSmallMax = kSortTile;
+constexpr size_t kSortSmem = kSortTile * 6 + kSortWarps * kMaxBins * 2 + kMaxBins * 4;
 
-// Entry i of segment `seg`: its key (b K + id), token and digit source; false past the segment's
-// end or for an id outside [0, K).
+// Entry i of segment `seg`: its key (b K + id) and token; false past the segment's end or for an id
+// outside [0, K).
 __device__ __forceinline__ bool sort_load(const SortSpec &s, uint32_t seg, uint32_t i, uint32_t &key, uint32_t &pos) {
     if (!s.keys) {
         if (i >= s.n) return false;
@@ -154,14 +155,16 @@ __device__ __forceinline__ bool sort_load(const SortSpec &s, uint32_t seg, uint3
     return true;
 }
 __device__ __forceinline__ uint32_t sort_digit(const SortSpec &s, uint32_t seg, uint32_t key) {
-    return ((s.by_batch ? key - seg * s.K : key) >> s.shift) & (s.bins - 1);
+    return ((s.by_batch ? key - seg * s.K : key) >> s.shift) & ((1u << s.width) - 1);
 }
 
-// Digit counts of each tile: counts[(seg * tps + tile) * bins + bin].
+// Digit counts of each tile: counts[(seg * tps + tile) * bins + bin]; the first pass also counts the
+// valid tokens of the segments (segtotal zeroed beforehand; integer sums do not depend on order).
 __global__ void __launch_bounds__(kSortThreads)
     sort_hist_kernel(const SortSpec s, uint32_t *__restrict__ counts) {
     __shared__ uint32_t bins[kMaxBins];
-    for (int b = threadIdx.x; b < s.bins; b += kSortThreads) bins[b] = 0;
+    const int nb = 1 << s.width;
+    if (threadIdx.x < nb) bins[threadIdx.x] = 0;
     __syncthreads();
     const uint32_t seg = blockIdx.x / s.tps, tile = blockIdx.x - seg * s.tps;
     uint32_t key[kSortItems], pos;
@@ -172,9 +175,15 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i)
         if (ok[i]) atomicAdd(&bins[sort_digit(s, seg, key[i])], 1u);
+    int valid = 0;
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) valid += ok[i];
     __syncthreads();
-    uint32_t *out = counts + static_cast<size_t>(blockIdx.x) * s.bins;
-    for (int b = threadIdx.x; b < s.bins; b += kSortThreads) out[b] = bins[b];
+    if (!s.keys) {
+        valid = __reduce_add_sync(0xffffffffu, valid);
+        if ((threadIdx.x & 31) == 0 && valid) atomicAdd(s.segtotal + seg, static_cast<uint32_t>(valid));
+    }
+    if (threadIdx.x < nb) counts[static_cast<size_t>(blockIdx.x) * nb + threadIdx.x] = bins[threadIdx.x];
 }
 
 // Exclusive scan of one value per thread over the block; *total receives the sum.
@@ -194,127 +203,150 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, 
         const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
     }
-    const uint32_t before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
+    const uint32_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
     *total = __shfl_sync(0xffffffffu, w, 31);
     __syncthreads();
-    return x - v + before;
+    return x - v + (warp ? before : 0);
 }
 
-// Tile counts -> exclusive scan over a segment's tiles, in place, and the totals per (segment,
-// bin); the block that finishes last scans the totals into the start of every (segment, bin) and
-// of every segment. A block covers 32 bins of a segment, its 32 warps a slice of the tiles each.
+// Many tiles: tile counts -> exclusive scan over a segment's tiles, in place, and the bins' sums. A
+// block covers 32 bins of a segment, its 32 warps a slice of the tiles each.
 __global__ void __launch_bounds__(1024)
-    sort_scan_kernel(const SortSpec s, uint32_t *__restrict__ counts, uint32_t *totals, uint32_t *segstart_out,
-                     unsigned int *done) {
+    sort_scan_kernel(const SortSpec s, uint32_t *__restrict__ counts, uint32_t *__restrict__ totals) {
     __shared__ uint32_t slice[32][33];
-    __shared__ uint32_t ws[32];
-    __shared__ bool last;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const uint32_t bpb = (s.bins + 31) / 32;
+    const uint32_t nb = 1u << s.width, bpb = (nb + 31) / 32;
     const uint32_t seg = blockIdx.x / bpb, bin = (blockIdx.x - seg * bpb) * 32 + lane;
-    const bool in = bin < static_cast<uint32_t>(s.bins);
-    uint32_t *c = counts + static_cast<size_t>(seg) * s.tps * s.bins + bin;
+    uint32_t *c = counts + static_cast<size_t>(seg) * s.tps * nb + bin;
     const uint32_t per = (s.tps + 31) / 32, a = min(s.tps, w * per), e = min(s.tps, a + per);
     uint32_t sum = 0;
-    if (in)
-        for (uint32_t t = a; t < e; ++t) sum += c[static_cast<size_t>(t) * s.bins];
+    if (bin < nb)
+        for (uint32_t t = a; t < e; ++t) sum += c[static_cast<size_t>(t) * nb];
     slice[w][lane] = sum;
     __syncthreads();
     uint32_t run = 0;
     for (int k = 0; k < w; ++k) run += slice[k][lane];
-    if (in) {
+    if (bin < nb) {
         for (uint32_t t = a; t < e; ++t) {
-            const uint32_t v = c[static_cast<size_t>(t) * s.bins];
-            c[static_cast<size_t>(t) * s.bins] = run;
+            const uint32_t v = c[static_cast<size_t>(t) * nb];
+            c[static_cast<size_t>(t) * nb] = run;
             run += v;
         }
-        if (w == 31) totals[seg * s.bins + bin] = run;
-    }
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(done, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    const uint32_t all = s.segs * s.bins;
-    uint32_t base = 0;
-    for (uint32_t i0 = 0; i0 < all; i0 += 4096) {
-        uint32_t v[4], own = 0;
-        const uint32_t i = i0 + threadIdx.x * 4;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = i + k < all ? __ldcg(totals + i + k) : 0;
-            own += v[k];
-        }
-        uint32_t tot, x = base + block_scan(own, ws, &tot);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + k < all) {
-                totals[i + k] = x;
-                if ((i + k) % s.bins == 0) segstart_out[(i + k) / s.bins] = x;
-                x += v[k];
-            }
-        base += tot;
-    }
-    if (threadIdx.x == 0) {
-        segstart_out[s.segs] = base;
-        *done = 0;
+        if (w == 31) totals[seg * nb + bin] = run;
     }
 }
 
-// Places every entry of a tile at (start of its bin) + (entries of the bin in earlier tiles) +
-// (earlier entries of the bin in this tile). Within a warp the rank among equal digits comes from
-// a match over 32 consecutive entries, so the order of equal digits is kept.
-__global__ void __launch_bounds__(kSortThreads)
-    sort_scatter_kernel(const SortSpec s, const uint32_t *__restrict__ counts, const uint32_t *__restrict__ starts,
+// Stable ranks of a warp's entries among equal digits: entry i of a lane is number i * 32 + lane of
+// the warp's. The lanes with an equal digit are found by a ballot per digit bit (a warp match has a
+// far lower rate). mine[bin] counts the warp's entries.
+template <int ITEMS>
+__device__ __forceinline__ void rank_digits(const uint32_t (&digit)[ITEMS], const bool (&ok)[ITEMS], int per, int width,
+                                            uint16_t *mine, uint16_t (&rank)[ITEMS]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        if (i >= per) break;
+        uint32_t peers = __ballot_sync(0xffffffffu, ok[i]);
+        for (int b = 0; b < width; ++b) {
+            const bool bit = (digit[i] >> b) & 1;
+            const uint32_t v = __ballot_sync(0xffffffffu, bit);
+            peers &= bit ? v : ~v;
+        }
+        uint32_t prior = 0;
+        if (ok[i]) prior = mine[digit[i]];
+        __syncwarp();
+        rank[i] = static_cast<uint16_t>(prior + __popc(peers & ((1u << lane) - 1)));
+        if (ok[i] && lane == __ffs(peers) - 1) mine[digit[i]] = static_cast<uint16_t>(prior + __popc(peers));
+        __syncwarp();
+    }
+}
+
+// Sorts a tile by the pass's digit in shared memory and writes its runs to (start of the bin) +
+// (entries of the bin in earlier tiles): consecutive threads write consecutive entries of a run.
+__global__ void __launch_bounds__(kSortThreads, 1)
+    sort_scatter_kernel(const SortSpec s, const uint32_t *__restrict__ counts, const uint32_t *__restrict__ totals,
                         uint32_t *__restrict__ keys_out, uint32_t *__restrict__ pos_out) {
     extern __shared__ uint32_t dyn[];
-    uint32_t *base = dyn;                                            // [bins]
-    uint16_t *wcount = reinterpret_cast<uint16_t *>(dyn + s.bins);   // [warps][bins]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ uint32_t ws[32];
+    uint32_t *skeys = dyn;                                                   // [tile]
+    uint16_t *sloc = reinterpret_cast<uint16_t *>(dyn + kSortTile);          // [tile]: number in the tile
+    uint16_t *wcount = sloc + kSortTile;                                     // [warps][bins]
+    uint32_t *shift_of = reinterpret_cast<uint32_t *>(wcount + kSortWarps * kMaxBins);   // [bins]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nb = 1 << s.width;
     const uint32_t seg = blockIdx.x / s.tps, tile = blockIdx.x - seg * s.tps;
-    const uint32_t i0 = tile * kSortTile + warp * (32 * kSortItems) + lane;
-    uint32_t key[kSortItems], pos[kSortItems];
+    const uint32_t i0 = warp * (32 * kSortItems) + lane;
+    uint32_t key[kSortItems], digit[kSortItems], pos;
     uint16_t rank[kSortItems];
     bool ok[kSortItems];
 #pragma unroll
-    for (int i = 0; i < kSortItems; ++i) ok[i] = sort_load(s, seg, i0 + i * 32, key[i], pos[i]);
-    const uint32_t *c = counts + static_cast<size_t>(blockIdx.x) * s.bins;
-    for (int b = threadIdx.x; b < s.bins; b += kSortThreads) {
-        base[b] = starts[seg * s.bins + b] + c[b];
-        for (int w = 0; w < kSortWarps; ++w) wcount[w * s.bins + b] = 0;
-    }
-    __syncthreads();
-    uint16_t *mine = wcount + warp * s.bins;
-#pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
-        const uint32_t digit = ok[i] ? sort_digit(s, seg, key[i]) : kMaxBins;
-        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-        uint32_t prior = 0;
-        if (ok[i]) prior = mine[digit];
-        __syncwarp();
-        rank[i] = static_cast<uint16_t>(prior + __popc(peers & ((1u << lane) - 1)));
-        if (ok[i] && lane == __ffs(peers) - 1) mine[digit] = static_cast<uint16_t>(prior + __popc(peers));
-        __syncwarp();
+        ok[i] = sort_load(s, seg, tile * kSortTile + i0 + i * 32, key[i], pos);
+        digit[i] = ok[i] ? sort_digit(s, seg, key[i]) : 0;
     }
-    __syncthreads();
-    for (int b = threadIdx.x; b < s.bins; b += kSortThreads) {
-        uint32_t run = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t v = wcount[w * s.bins + b];
-            wcount[w * s.bins + b] = static_cast<uint16_t>(run);
-            run += v;
+    // valid tokens of earlier segments
+    uint32_t before = 0, all = 0;
+    for (uint32_t k = threadIdx.x; k < s.segs; k += kSortThreads) {
+        const uint32_t v = s.segtotal[k];
+        all += v;
+        if (k < seg) before += v;
+    }
+    uint32_t segbase, sum;
+    block_scan(before, ws, &segbase);
+    block_scan(all, ws, &sum);
+    if (!s.keys && tile == 0 && threadIdx.x == 0) {
+        s.segstart[seg] = segbase;
+        if (seg == 0) s.segstart[s.segs] = sum;
+    }
+    // this thread's bin: entries in earlier tiles and in all of the segment
+    uint32_t early = 0, whole = 0;
+    if (threadIdx.x < nb) {
+        const uint32_t *c = counts + static_cast<size_t>(seg) * s.tps * nb + threadIdx.x;
+        if (s.scanned) {
+            early = c[static_cast<size_t>(tile) * nb];
+            whole = totals[seg * nb + threadIdx.x];
+        } else {
+#pragma unroll 4
+            for (uint32_t t = 0; t < s.tps; ++t) {
+                const uint32_t v = c[static_cast<size_t>(t) * nb];
+                if (t < tile) early += v;
+                whole += v;
+            }
         }
+    }
+    const uint32_t start = segbase + block_scan(whole, ws, &sum) + early;
+    for (int k = threadIdx.x; k < kSortWarps * nb / 2; k += kSortThreads) reinterpret_cast<uint32_t *>(wcount)[k] = 0;
+    __syncthreads();
+    uint16_t *mine = wcount + warp * nb;
+    rank_digits<kSortItems>(digit, ok, kSortItems, s.width, mine, rank);
+    __syncthreads();
+    uint32_t count = 0;
+    if (threadIdx.x < nb)
+        for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t v = wcount[w * nb + threadIdx.x];
+            wcount[w * nb + threadIdx.x] = static_cast<uint16_t>(count);
+            count += v;
+        }
+    uint32_t entries;
+    const uint32_t local = block_scan(count, ws, &entries);      // the bin's place in the sorted tile
+    if (threadIdx.x < nb) {
+        shift_of[threadIdx.x] = start - local;
+        for (int w = 0; w < kSortWarps; ++w) wcount[w * nb + threadIdx.x] += static_cast<uint16_t>(local);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i)
         if (ok[i]) {
-            const uint32_t digit = sort_digit(s, seg, key[i]);
-            const uint32_t at = base[digit] + mine[digit] + rank[i];
-            keys_out[at] = key[i];
-            pos_out[at] = pos[i];
+            const uint32_t at = mine[digit[i]] + rank[i];
+            skeys[at] = key[i];
+            sloc[at] = static_cast<uint16_t>(i0 + i * 32);
         }
+    __syncthreads();
+    const uint32_t from = s.keys ? s.segstart[seg] + tile * kSortTile : seg * s.n + tile * kSortTile;
+    for (uint32_t at = threadIdx.x; at < entries; at += kSortThreads) {
+        const uint32_t k = skeys[at], to = at + shift_of[sort_digit(s, seg, k)];
+        keys_out[to] = k;
+        pos_out[to] = s.keys ? s.pos[from + sloc[at]] : from + sloc[at];
+    }
 }
 
 // Zeros over [p, p + bytes), spread over `threads` threads of which this is number i.
@@ -329,105 +361,86 @@ __device__ __forceinline__ void zero_fill(uint8_t *p, size_t bytes, size_t i, si
     if (tail + i < bytes) p[tail + i] = 0;
 }
 
-// Up to kSmallMax tokens: block 0 sorts them in shared memory (digits of at most 9 bits; dropped
-// tokens carry the key B K and end up behind the others) while the other blocks zero the table's
-// gradient, which for a large table takes longer than the sort.
-__global__ void __launch_bounds__(kSmallThreads, 1)
-    sort_small_kernel(const SortSpec s, uint32_t tokens, uint32_t keys_total, int passes, int width,
+// Up to kSmallMax tokens: block 0 sorts them in shared memory (dropped tokens carry the key B K and
+// end up behind the others) while the other blocks zero the table's gradient, which for a large
+// table takes longer than the sort.
+__global__ void __launch_bounds__(kSortThreads, 1)
+    sort_small_kernel(const SortSpec s, uint32_t tokens, uint32_t keys_total, int passes,
                       uint32_t *__restrict__ keys_out, uint32_t *__restrict__ pos_out, uint32_t *__restrict__ nvalid,
                       unsigned int *__restrict__ jobs, uint8_t *zero, size_t zero_bytes) {
     if (blockIdx.x > 0) {
         if (zero)
-            zero_fill(zero, zero_bytes, static_cast<size_t>(blockIdx.x - 1) * kSmallThreads + threadIdx.x,
-                      static_cast<size_t>(gridDim.x - 1) * kSmallThreads);
+            zero_fill(zero, zero_bytes, static_cast<size_t>(blockIdx.x - 1) * kSortThreads + threadIdx.x,
+                      static_cast<size_t>(gridDim.x - 1) * kSortThreads);
         return;
     }
     extern __shared__ uint32_t dyn[];
     __shared__ uint32_t ws[32];
     uint32_t *skeys = dyn;                                                   // [kSmallMax]
     uint16_t *spos = reinterpret_cast<uint16_t *>(dyn + kSmallMax);          // [kSmallMax]
-    uint16_t *wcount = spos + kSmallMax;                                     // [32][kSmallBins]
-    uint32_t *base = reinterpret_cast<uint32_t *>(wcount + 32 * kSmallBins);  // [kSmallBins]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = static_cast<int>((tokens + kSmallThreads - 1) / kSmallThreads);
+    uint16_t *wcount = spos + kSmallMax;                                     // [warps][bins]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nb = 1 << s.width;
+    const int per = static_cast<int>((tokens + kSortThreads - 1) / kSortThreads);
     const uint32_t i0 = static_cast<uint32_t>(warp * 32 * per + lane);
-    uint32_t key[kSmallItems];
-    uint16_t pos[kSmallItems], rank[kSmallItems];
-    int valid = 0;
+    uint32_t key[kSortItems], digit[kSortItems];
+    uint16_t pos[kSortItems], rank[kSortItems];
+    bool ok[kSortItems];
+    uint32_t valid = 0;
 #pragma unroll
-    for (int i = 0; i < kSmallItems; ++i)
-        if (i < per) {
-            const uint32_t at = i0 + i * 32;
-            pos[i] = static_cast<uint16_t>(at);
-            key[i] = 0xffffffffu;                 // no entry at all
-            if (at < tokens) {
-                const uint32_t id = static_cast<uint32_t>(s.ids[at]);
-                key[i] = id < s.K ? fd_div(s.divN, at) * s.K + id : keys_total;
-                valid += id < s.K;
-            }
-        }
-    {
-        uint32_t tot;
-        block_scan(static_cast<uint32_t>(valid), ws, &tot);
-        if (threadIdx.x == 0) {
-            *nvalid = tot;
-            *jobs = 0;
+    for (int i = 0; i < kSortItems; ++i) {
+        const uint32_t at = i0 + i * 32;
+        ok[i] = i < per && at < tokens;
+        pos[i] = static_cast<uint16_t>(at);
+        if (ok[i]) {
+            const uint32_t id = static_cast<uint32_t>(s.ids[at]);
+            key[i] = id < s.K ? fd_div(s.divN, at) * s.K + id : keys_total;
+            valid += id < s.K;
         }
     }
-    const int bins = 1 << width;
-    uint16_t *mine = wcount + warp * kSmallBins;
+    uint32_t tot;
+    block_scan(valid, ws, &tot);
+    if (threadIdx.x == 0) {
+        *nvalid = tot;
+        *jobs = 0;
+    }
+    uint16_t *mine = wcount + warp * nb;
     for (int pass = 0; pass < passes; ++pass) {
-        const int shift = pass * width;
-        for (int b = threadIdx.x; b < 32 * kSmallBins / 2; b += kSmallThreads) reinterpret_cast<uint32_t *>(wcount)[b] = 0;
+        for (int k = threadIdx.x; k < kSortWarps * nb / 2; k += kSortThreads) reinterpret_cast<uint32_t *>(wcount)[k] = 0;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSmallItems; ++i)
-            if (i < per) {
-                const bool ok = i0 + i * 32 < tokens;
-                const uint32_t digit = ok ? (key[i] >> shift) & (bins - 1) : kSmallBins;
-                const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-                uint32_t prior = 0;
-                if (ok) prior = mine[digit];
-                __syncwarp();
-                rank[i] = static_cast<uint16_t>(prior + __popc(peers & ((1u << lane) - 1)));
-                if (ok && lane == __ffs(peers) - 1) mine[digit] = static_cast<uint16_t>(prior + __popc(peers));
-                __syncwarp();
-            }
+        for (int i = 0; i < kSortItems; ++i) digit[i] = ok[i] ? (key[i] >> (pass * s.width)) & (nb - 1) : 0;
+        rank_digits<kSortItems>(digit, ok, per, s.width, mine, rank);
         __syncthreads();
         uint32_t sum = 0;
-        if (threadIdx.x < bins)
-            for (int w = 0; w < 32; ++w) {
-                const uint32_t v = wcount[w * kSmallBins + threadIdx.x];
-                wcount[w * kSmallBins + threadIdx.x] = static_cast<uint16_t>(sum);
+        if (threadIdx.x < nb)
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t v = wcount[w * nb + threadIdx.x];
+                wcount[w * nb + threadIdx.x] = static_cast<uint16_t>(sum);
                 sum += v;
             }
-        uint32_t tot;
         const uint32_t start = block_scan(sum, ws, &tot);
-        if (threadIdx.x < bins) base[threadIdx.x] = start;
+        if (threadIdx.x < nb)
+            for (int w = 0; w < kSortWarps; ++w) wcount[w * nb + threadIdx.x] += static_cast<uint16_t>(start);
         __syncthreads();
-        const bool final = pass + 1 == passes;
 #pragma unroll
-        for (int i = 0; i < kSmallItems; ++i)
-            if (i < per && i0 + i * 32 < tokens) {
-                const uint32_t digit = (key[i] >> shift) & (bins - 1);
-                const uint32_t at = base[digit] + mine[digit] + rank[i];
-                if (final) {
-                    keys_out[at] = key[i];
-                    pos_out[at] = pos[i];
-                } else {
-                    skeys[at] = key[i];
-                    spos[at] = pos[i];
-                }
+        for (int i = 0; i < kSortItems; ++i)
+            if (ok[i]) {
+                const uint32_t at = mine[digit[i]] + rank[i];
+                skeys[at] = key[i];
+                spos[at] = pos[i];
             }
-        if (final) break;
         __syncthreads();
+        if (pass + 1 == passes) break;
 #pragma unroll
-        for (int i = 0; i < kSmallItems; ++i)
-            if (i < per && i0 + i * 32 < tokens) {
+        for (int i = 0; i < kSortItems; ++i)
+            if (ok[i]) {
                 key[i] = skeys[i0 + i * 32];
                 pos[i] = spos[i0 + i * 32];
             }
-        __syncthreads();
+    }
+    for (uint32_t at = threadIdx.x; at < tokens; at += kSortThreads) {
+        keys_out[at] = skeys[at];
+        pos_out[at] = spos[at];
     }
 }
 
@@ -718,19 +731,19 @@ inline SortPlan sort_plan(int64_t B, int64_t N, int64_t K) {
     p.small = B * N <= kSmallMax;
     if (p.small) {
         const int bits = bits_of(B * K + 1);
-        p.passes = static_cast<int>(ceil_div(bits, 9));
+        p.passes = static_cast<int>(ceil_div(bits, kMaxWidth));
         p.width = static_cast<int>(ceil_div(bits, p.passes));
         return p;
     }
-    // Batches of at least half a tile are segments (their sort needs the bits of the id alone), as
-    // long as one block can scan the starts of all their bins.
+    // Batches of at least half a tile are segments (their sort needs the bits of the id alone; every
+    // block sums the sizes of the segments before its own).
     int bits = bits_of(K);
-    p.passes = static_cast<int>(ceil_div(bits, 11));
+    p.passes = static_cast<int>(ceil_div(bits, kMaxWidth));
     p.width = static_cast<int>(ceil_div(bits, p.passes));
-    p.by_batch = N >= kSortTile / 2 && (B << p.width) <= 65536;
+    p.by_batch = N >= kSortTile / 2 && B <= 65536;
     if (!p.by_batch) {
         bits = bits_of(B * K);
-        p.passes = static_cast<int>(ceil_div(bits, 11));
+        p.passes = static_cast<int>(ceil_div(bits, kMaxWidth));
         p.width = static_cast<int>(ceil_div(bits, p.passes));
     }
     p.segs = p.by_batch ? B : 1;
@@ -744,8 +757,7 @@ inline SortPlan sort_plan(int64_t B, int64_t N, int64_t K) {
 inline int64_t grad_range(int64_t T) { return std::max<int64_t>(16, ceil_div(T, 148 * 64)); }
 
 struct GradWs {
-    uint32_t *keys[2], *pos[2], *counts, *totals, *segstart, *jobs;
-    unsigned int *done;
+    uint32_t *keys[2], *pos[2], *counts, *totals, *segtotal, *segstart, *jobs;
     float *slots;
 };
 inline GradWs carve_grad(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d) {
@@ -758,10 +770,10 @@ inline GradWs carve_grad(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d) 
     }
     if (!p.small) {
         g.counts = c.take<uint32_t>(static_cast<size_t>(p.segs * p.tps << p.width) * 4);
-        g.totals = c.take<uint32_t>(static_cast<size_t>(p.segs << p.width) * 4);
+        if (p.tps > kScanTiles) g.totals = c.take<uint32_t>(static_cast<size_t>(p.segs << p.width) * 4);
+        g.segtotal = c.take<uint32_t>(static_cast<size_t>(p.segs) * 4);
     }
-    g.segstart = c.take<uint32_t>(static_cast<size_t>(std::max<int64_t>(p.segs, 0) + 1) * 4);
-    g.done = c.take<unsigned int>(4);
+    g.segstart = c.take<uint32_t>(static_cast<size_t>(p.segs + 1) * 4);
     g.jobs = c.take<uint32_t>(static_cast<size_t>(ranges + 1) * 4);
     g.slots = c.take<float>(static_cast<size_t>(ranges * 2 * d) * 4);
     return g;
@@ -779,32 +791,35 @@ km_status grad_sort(const int32_t *ids, int64_t B, int64_t N, int64_t K, const G
     SortSpec s = {};
     s.ids = ids;
     s.divN = make_fastdiv(static_cast<uint32_t>(N));
-    s.N = static_cast<uint32_t>(N);
     s.K = static_cast<uint32_t>(K);
+    s.width = p.width;
     if (p.small) {
-        constexpr int kSmem = kSmallMax * 6 + 32 * kSmallBins * 2 + kSmallBins * 4;
-        if (cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kSortSmem)) != cudaSuccess)
             return KM_ERR_CUDA;
         // a zeroing block per 64 KB, one per SM at most
-        const int64_t fill = zero ? std::min<int64_t>(num_sms() - 1, ceil_div(static_cast<int64_t>(zero_bytes), 65536)) : 0;
-        sort_small_kernel<<<static_cast<unsigned>(1 + fill), kSmallThreads, kSmem, st>>>(
-            s, static_cast<uint32_t>(T), static_cast<uint32_t>(B * K), p.passes, p.width, w.keys[0], w.pos[0], w.segstart,
-            w.jobs, static_cast<uint8_t *>(zero), zero_bytes);
+        const int64_t fill = zero ? std::min<int64_t>(std::max(1, num_sms() - 1), ceil_div(static_cast<int64_t>(zero_bytes), 65536)) : 0;
+        sort_small_kernel<<<static_cast<unsigned>(1 + fill), kSortThreads, kSortSmem, st>>>(
+            s, static_cast<uint32_t>(T), static_cast<uint32_t>(B * K), p.passes, w.keys[0], w.pos[0], w.segstart, w.jobs,
+            static_cast<uint8_t *>(zero), zero_bytes);
         *side = 0;
         *nvalid = w.segstart;
         return launch_status();
     }
     if ((zero && cudaMemsetAsync(zero, 0, zero_bytes, st) != cudaSuccess) ||
-        cudaMemsetAsync(w.done, 0, 4, st) != cudaSuccess || cudaMemsetAsync(w.jobs, 0, 4, st) != cudaSuccess ||
+        cudaMemsetAsync(w.segtotal, 0, static_cast<size_t>(p.segs) * 4, st) != cudaSuccess ||
+        cudaMemsetAsync(w.jobs, 0, 4, st) != cudaSuccess ||
         cudaFuncSetAttribute(sort_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxBins * (4 + 2 * kSortWarps)) != cudaSuccess)
+                             static_cast<int>(kSortSmem)) != cudaSuccess)
         return KM_ERR_CUDA;
     s.n = static_cast<uint32_t>(p.n);
     s.segs = static_cast<uint32_t>(p.segs);
     s.tps = static_cast<uint32_t>(p.tps);
-    s.bins = 1 << p.width;
     s.by_batch = p.by_batch ? 1 : 0;
-    const int64_t blocks = p.segs * p.tps, sblocks = p.segs * ceil_div(s.bins, 32);
+    s.scanned = p.tps > kScanTiles ? 1 : 0;
+    s.segtotal = w.segtotal;
+    s.segstart = w.segstart;
+    const int64_t blocks = p.segs * p.tps, sblocks = p.segs * ceil_div(int64_t{1} << p.width, 32);
     if (blocks > kMaxIndex || sblocks > kMaxIndex) return KM_ERR_UNSUPPORTED;
     *side = 0;
     for (int pass = 0; pass < p.passes; ++pass) {
@@ -812,14 +827,15 @@ km_status grad_sort(const int32_t *ids, int64_t B, int64_t N, int64_t K, const G
         if (pass) {
             s.keys = w.keys[*side];
             s.pos = w.pos[*side];
-            s.segstart = w.segstart;
             *side ^= 1;
         }
         sort_hist_kernel<<<static_cast<unsigned>(blocks), kSortThreads, 0, st>>>(s, w.counts);
         if (launch_status() != KM_OK) return KM_ERR_CUDA;
-        sort_scan_kernel<<<static_cast<unsigned>(sblocks), 1024, 0, st>>>(s, w.counts, w.totals, w.segstart, w.done);
-        if (launch_status() != KM_OK) return KM_ERR_CUDA;
-        sort_scatter_kernel<<<static_cast<unsigned>(blocks), kSortThreads, s.bins * (4 + 2 * kSortWarps), st>>>(
+        if (s.scanned) {
+            sort_scan_kernel<<<static_cast<unsigned>(sblocks), 1024, 0, st>>>(s, w.counts, w.totals);
+            if (launch_status() != KM_OK) return KM_ERR_CUDA;
+        }
+        sort_scatter_kernel<<<static_cast<unsigned>(blocks), kSortThreads, kSortSmem, st>>>(
             s, w.counts, w.totals, w.keys[*side], w.pos[*side]);
         if (launch_status() != KM_OK) return KM_ERR_CUDA;
     }
