@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kLookupThreads)
 // least-significant-digit radix sort over the id's bits, digits of up to 10 bits. Where every
 // batch is long, batches are segments that are sorted side by side on the id alone (their order
 // is already that of the keys); where batches are short, all tokens are one segment with keys
-// b K + id. Up to kSmallMax tokens one block sorts everything in shared memory.
+// b K + id. Up to kSmallMax tokens a cluster of blocks sorts everything in its shared memory.
 
 struct SortSpec {
     const int32_t *ids;
@@ -126,16 +126,18 @@ struct SortSpec {
     const uint32_t *keys, *pos;   // entries of the pass before (first pass: null)
     uint32_t *segtotal;      // [segs] valid tokens
     uint32_t *segstart;      // [segs + 1] their exclusive sums (written by the first scatter)
+    FastDiv divE;            // entries per block of the sorting cluster
 };
 
-constexpr int kSortThreads = 1024;
+constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortItems = 16;
 constexpr int kSortTile = kSortThreads * kSortItems;
 constexpr int kMaxWidth = 10;                  // bits of a digit
 constexpr int kMaxBins = 1 << kMaxWidth;
 constexpr int kScanTiles = 64;                 // above this many tiles a kernel of its own scans them
-constexpr int kSmallMax = kSortTile;
+constexpr int kCluster = 8;
+constexpr int kSmallMax = kCluster * kSortTile;
 constexpr size_t kSortSmem = kSortTile * 6 + kSortWarps * kMaxBins * 2 + kMaxBins * 4;
 
 // Entry i of segment `seg`: its key (b K + id) and token; false past the segment's end or for an id
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kSortThreads)
     sort_hist_kernel(const SortSpec s, uint32_t *__restrict__ counts) {
     __shared__ uint32_t bins[kMaxBins];
     const int nb = 1 << s.width;
-    if (threadIdx.x < nb) bins[threadIdx.x] = 0;
+    for (int b = threadIdx.x; b < nb; b += kSortThreads) bins[b] = 0;
     __syncthreads();
     const uint32_t seg = blockIdx.x / s.tps, tile = blockIdx.x - seg * s.tps;
     uint32_t key[kSortItems], pos;
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kSortThreads)
         valid = __reduce_add_sync(0xffffffffu, valid);
         if ((threadIdx.x & 31) == 0 && valid) atomicAdd(s.segtotal + seg, static_cast<uint32_t>(valid));
     }
-    if (threadIdx.x < nb) counts[static_cast<size_t>(blockIdx.x) * nb + threadIdx.x] = bins[threadIdx.x];
+    for (int b = threadIdx.x; b < nb; b += kSortThreads) counts[static_cast<size_t>(blockIdx.x) * nb + b] = bins[b];
 }
 
 // Exclusive scan of one value per thread over the block; *total receives the sum.
@@ -238,32 +240,67 @@ __global__ void __launch_bounds__(1024)
 
 // Stable ranks of a warp's entries among equal digits: entry i of a lane is number i * 32 + lane of
 // the warp's. The lanes with an equal digit are found by a ballot per digit bit (a warp match has a
-// far lower rate). mine[bin] counts the warp's entries.
-template <int ITEMS>
-__device__ __forceinline__ void rank_digits(const uint32_t (&digit)[ITEMS], const bool (&ok)[ITEMS], int per, int width,
-                                            uint16_t *mine, uint16_t (&rank)[ITEMS]) {
+// far lower rate), for all entries first: the ballots do not depend on one another, the counting
+// that follows does. mine[bin] counts the warp's entries.
+__device__ __forceinline__ void rank_digits(const uint32_t (&digit)[kSortItems], const bool (&ok)[kSortItems], int per,
+                                            uint16_t *mine, uint16_t (&rank)[kSortItems]) {
     const int lane = threadIdx.x & 31;
+    uint32_t peers[kSortItems];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
+    for (int i = 0; i < kSortItems; ++i) {
         if (i >= per) break;
-        uint32_t peers = __ballot_sync(0xffffffffu, ok[i]);
-        for (int b = 0; b < width; ++b) {
+        uint32_t p = __ballot_sync(0xffffffffu, ok[i]);
+#pragma unroll
+        for (int b = 0; b < kMaxWidth; ++b) {
             const bool bit = (digit[i] >> b) & 1;
             const uint32_t v = __ballot_sync(0xffffffffu, bit);
-            peers &= bit ? v : ~v;
+            p &= bit ? v : ~v;
         }
+        peers[i] = p;
+    }
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+        if (i >= per) break;
         uint32_t prior = 0;
         if (ok[i]) prior = mine[digit[i]];
         __syncwarp();
-        rank[i] = static_cast<uint16_t>(prior + __popc(peers & ((1u << lane) - 1)));
-        if (ok[i] && lane == __ffs(peers) - 1) mine[digit[i]] = static_cast<uint16_t>(prior + __popc(peers));
+        rank[i] = static_cast<uint16_t>(prior + __popc(peers[i] & ((1u << lane) - 1)));
+        if (ok[i] && lane == __ffs(peers[i]) - 1) mine[digit[i]] = static_cast<uint16_t>(prior + __popc(peers[i]));
         __syncwarp();
     }
 }
 
+// The warps' counts of one bin: their sum, each replaced by the sum of the ones before it plus `add`.
+__device__ __forceinline__ uint32_t scan_warps(uint16_t *wcount, int nb, int bin, uint32_t add) {
+    uint32_t v[kSortWarps];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) v[w] = wcount[w * nb + bin];
+    uint32_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        wcount[w * nb + bin] = static_cast<uint16_t>(sum + add);
+        sum += v[w];
+    }
+    return sum;
+}
+__device__ __forceinline__ uint32_t sum_warps(const uint16_t *wcount, int nb, int bin) {
+    uint32_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) sum += wcount[w * nb + bin];
+    return sum;
+}
+constexpr int kBinsPerThread = kMaxBins / kSortThreads;
+// Exclusive sums over all bins of one value per bin; thread t holds bins 2 t and 2 t + 1.
+static_assert(kBinsPerThread == 2, "block_scan_bins pairs the bins");
+__device__ __forceinline__ void block_scan_bins(uint32_t (&v)[2], uint32_t *ws, uint32_t *total) {
+    const uint32_t a = v[0], x = block_scan(v[0] + v[1], ws, total);
+    v[0] = x;
+    v[1] = x + a;
+}
+
 // Sorts a tile by the pass's digit in shared memory and writes its runs to (start of the bin) +
 // (entries of the bin in earlier tiles): consecutive threads write consecutive entries of a run.
-__global__ void __launch_bounds__(kSortThreads, 1)
+__global__ void __launch_bounds__(kSortThreads)
     sort_scatter_kernel(const SortSpec s, const uint32_t *__restrict__ counts, const uint32_t *__restrict__ totals,
                         uint32_t *__restrict__ keys_out, uint32_t *__restrict__ pos_out) {
     extern __shared__ uint32_t dyn[];
@@ -283,6 +320,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         ok[i] = sort_load(s, seg, tile * kSortTile + i0 + i * 32, key[i], pos);
         digit[i] = ok[i] ? sort_digit(s, seg, key[i]) : 0;
     }
+    for (int k = threadIdx.x; k < kSortWarps * nb / 2; k += kSortThreads) reinterpret_cast<uint32_t *>(wcount)[k] = 0;
     // valid tokens of earlier segments
     uint32_t before = 0, all = 0;
     for (uint32_t k = threadIdx.x; k < s.segs; k += kSortThreads) {
@@ -297,40 +335,40 @@ __global__ void __launch_bounds__(kSortThreads, 1)
         s.segstart[seg] = segbase;
         if (seg == 0) s.segstart[s.segs] = sum;
     }
-    // this thread's bin: entries in earlier tiles and in all of the segment
-    uint32_t early = 0, whole = 0;
-    if (threadIdx.x < nb) {
-        const uint32_t *c = counts + static_cast<size_t>(seg) * s.tps * nb + threadIdx.x;
+    // this thread's bins: entries in earlier tiles and in all of the segment
+    uint32_t early[2] = {0, 0}, whole[2] = {0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int bin = threadIdx.x * 2 + h;
+        if (bin >= nb) continue;
+        const uint32_t *c = counts + static_cast<size_t>(seg) * s.tps * nb + bin;
         if (s.scanned) {
-            early = c[static_cast<size_t>(tile) * nb];
-            whole = totals[seg * nb + threadIdx.x];
+            early[h] = c[static_cast<size_t>(tile) * nb];
+            whole[h] = totals[seg * nb + bin];
         } else {
-#pragma unroll 4
+#pragma unroll 8
             for (uint32_t t = 0; t < s.tps; ++t) {
                 const uint32_t v = c[static_cast<size_t>(t) * nb];
-                if (t < tile) early += v;
-                whole += v;
+                if (t < tile) early[h] += v;
+                whole[h] += v;
             }
         }
     }
-    const uint32_t start = segbase + block_scan(whole, ws, &sum) + early;
-    for (int k = threadIdx.x; k < kSortWarps * nb / 2; k += kSortThreads) reinterpret_cast<uint32_t *>(wcount)[k] = 0;
-    __syncthreads();
+    block_scan_bins(whole, ws, &sum);            // (its barriers also cover the zeroed counters)
     uint16_t *mine = wcount + warp * nb;
-    rank_digits<kSortItems>(digit, ok, kSortItems, s.width, mine, rank);
+    rank_digits(digit, ok, kSortItems, mine, rank);
     __syncthreads();
-    uint32_t count = 0;
-    if (threadIdx.x < nb)
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t v = wcount[w * nb + threadIdx.x];
-            wcount[w * nb + threadIdx.x] = static_cast<uint16_t>(count);
-            count += v;
-        }
-    uint32_t entries;
-    const uint32_t local = block_scan(count, ws, &entries);      // the bin's place in the sorted tile
-    if (threadIdx.x < nb) {
-        shift_of[threadIdx.x] = start - local;
-        for (int w = 0; w < kSortWarps; ++w) wcount[w * nb + threadIdx.x] += static_cast<uint16_t>(local);
+    uint32_t local[2] = {0, 0}, entries;         // the bins' places in the sorted tile
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (threadIdx.x * 2 + h < nb) local[h] = sum_warps(wcount, nb, threadIdx.x * 2 + h);
+    block_scan_bins(local, ws, &entries);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int bin = threadIdx.x * 2 + h;
+        if (bin >= nb) continue;
+        scan_warps(wcount, nb, bin, local[h]);
+        shift_of[bin] = segbase + whole[h] + early[h] - local[h];
     }
     __syncthreads();
 #pragma unroll
@@ -361,36 +399,65 @@ __device__ __forceinline__ void zero_fill(uint8_t *p, size_t bytes, size_t i, si
     if (tail + i < bytes) p[tail + i] = 0;
 }
 
-// Up to kSmallMax tokens: block 0 sorts them in shared memory (dropped tokens carry the key B K and
-// end up behind the others) while the other blocks zero the table's gradient, which for a large
-// table takes longer than the sort.
-__global__ void __launch_bounds__(kSortThreads, 1)
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_load(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_store2(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+
+constexpr size_t kSmallSmem = kSortTile * 8 + kSortWarps * kMaxBins * 2 + kMaxBins * 4;
+
+// Up to kSmallMax tokens in one launch: the first cluster of eight blocks sorts, exchanging digit
+// counts and entries through its blocks' shared memory (dropped tokens carry the key B K and end up
+// behind the others); the other blocks zero the table's gradient, which for a large table takes
+// longer than the sort. Block c of the cluster holds entries [c E, (c + 1) E).
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads, 1)
     sort_small_kernel(const SortSpec s, uint32_t tokens, uint32_t keys_total, int passes,
                       uint32_t *__restrict__ keys_out, uint32_t *__restrict__ pos_out, uint32_t *__restrict__ nvalid,
                       unsigned int *__restrict__ jobs, uint8_t *zero, size_t zero_bytes) {
-    if (blockIdx.x > 0) {
+    if (blockIdx.x >= kCluster) {
         if (zero)
-            zero_fill(zero, zero_bytes, static_cast<size_t>(blockIdx.x - 1) * kSortThreads + threadIdx.x,
-                      static_cast<size_t>(gridDim.x - 1) * kSortThreads);
+            zero_fill(zero, zero_bytes, static_cast<size_t>(blockIdx.x - kCluster) * kSortThreads + threadIdx.x,
+                      static_cast<size_t>(gridDim.x - kCluster) * kSortThreads);
         return;
     }
     extern __shared__ uint32_t dyn[];
     __shared__ uint32_t ws[32];
-    uint32_t *skeys = dyn;                                                   // [kSmallMax]
-    uint16_t *spos = reinterpret_cast<uint16_t *>(dyn + kSmallMax);          // [kSmallMax]
-    uint16_t *wcount = spos + kSmallMax;                                     // [warps][bins]
+    __shared__ uint32_t nvalid_mine;
+    uint2 *entries = reinterpret_cast<uint2 *>(dyn);                                 // [E]: key, token
+    uint16_t *wcount = reinterpret_cast<uint16_t *>(dyn + 2 * kSortTile);            // [warps][bins]
+    uint32_t *bincount = reinterpret_cast<uint32_t *>(wcount + kSortWarps * kMaxBins);   // [bins], this block's
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nb = 1 << s.width;
-    const int per = static_cast<int>((tokens + kSortThreads - 1) / kSortThreads);
+    const uint32_t rank_c = cluster_rank();
+    const int per = static_cast<int>((tokens + kCluster * kSortThreads - 1) / (kCluster * kSortThreads));
+    const uint32_t E = static_cast<uint32_t>(per) * kSortThreads, e0 = rank_c * E;
+    const FastDiv div_e = s.divE;
     const uint32_t i0 = static_cast<uint32_t>(warp * 32 * per + lane);
-    uint32_t key[kSortItems], digit[kSortItems];
-    uint16_t pos[kSortItems], rank[kSortItems];
+    uint32_t key[kSortItems], pos[kSortItems], digit[kSortItems];
+    uint16_t rank[kSortItems];
     bool ok[kSortItems];
     uint32_t valid = 0;
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
-        const uint32_t at = i0 + i * 32;
+        const uint32_t at = e0 + i0 + i * 32;
         ok[i] = i < per && at < tokens;
-        pos[i] = static_cast<uint16_t>(at);
+        pos[i] = at;
         if (ok[i]) {
             const uint32_t id = static_cast<uint32_t>(s.ids[at]);
             key[i] = id < s.K ? fd_div(s.divN, at) * s.K + id : keys_total;
@@ -399,48 +466,75 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     }
     uint32_t tot;
     block_scan(valid, ws, &tot);
-    if (threadIdx.x == 0) {
-        *nvalid = tot;
-        *jobs = 0;
-    }
+    if (threadIdx.x == 0) nvalid_mine = tot;
     uint16_t *mine = wcount + warp * nb;
     for (int pass = 0; pass < passes; ++pass) {
         for (int k = threadIdx.x; k < kSortWarps * nb / 2; k += kSortThreads) reinterpret_cast<uint32_t *>(wcount)[k] = 0;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) digit[i] = ok[i] ? (key[i] >> (pass * s.width)) & (nb - 1) : 0;
-        rank_digits<kSortItems>(digit, ok, per, s.width, mine, rank);
+        rank_digits(digit, ok, per, mine, rank);
         __syncthreads();
-        uint32_t sum = 0;
-        if (threadIdx.x < nb)
-            for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t v = wcount[w * nb + threadIdx.x];
-                wcount[w * nb + threadIdx.x] = static_cast<uint16_t>(sum);
-                sum += v;
+        for (int b = threadIdx.x; b < nb; b += kSortThreads) bincount[b] = sum_warps(wcount, nb, b);
+        cluster_sync();
+        // entries of this thread's bins in earlier blocks and in all
+        uint32_t early[2] = {0, 0}, whole[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c) {
+            const uint32_t base = cluster_addr(bincount, c);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int bin = threadIdx.x * 2 + h;
+                const uint32_t v = bin < nb ? cluster_load(base + bin * 4) : 0;
+                if (c < static_cast<int>(rank_c)) early[h] += v;
+                whole[h] += v;
             }
-        const uint32_t start = block_scan(sum, ws, &tot);
-        if (threadIdx.x < nb)
-            for (int w = 0; w < kSortWarps; ++w) wcount[w * nb + threadIdx.x] += static_cast<uint16_t>(start);
+        }
+        if (pass == 0 && rank_c == 0 && threadIdx.x < 32) {
+            const uint32_t v = lane < kCluster ? cluster_load(cluster_addr(&nvalid_mine, lane)) : 0;
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, v);
+            if (lane == 0) {
+                *nvalid = sum;
+                *jobs = 0;
+            }
+        }
+        block_scan_bins(whole, ws, &tot);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int bin = threadIdx.x * 2 + h;
+            // the warps' places relative to the block's first entry of the bin (16 bits), and that
+            if (bin < nb) scan_warps(wcount, nb, bin, 0);
+        }
+        // every block has read the counts; then they hold the bins' starts of this block
+        cluster_sync();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int bin = threadIdx.x * 2 + h;
+            if (bin < nb) bincount[bin] = whole[h] + early[h];
+        }
         __syncthreads();
+        const bool final = pass + 1 == passes;
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i)
             if (ok[i]) {
-                const uint32_t at = mine[digit[i]] + rank[i];
-                skeys[at] = key[i];
-                spos[at] = pos[i];
+                const uint32_t at = bincount[digit[i]] + mine[digit[i]] + rank[i];
+                if (final) {
+                    keys_out[at] = key[i];
+                    pos_out[at] = pos[i];
+                } else {
+                    const uint32_t c = fd_div(div_e, at);
+                    cluster_store2(cluster_addr(entries + (at - c * E), c), key[i], pos[i]);
+                }
             }
-        __syncthreads();
-        if (pass + 1 == passes) break;
+        cluster_sync();          // the entries have arrived; nobody leaves while others still read
+        if (final) break;
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i)
             if (ok[i]) {
-                key[i] = skeys[i0 + i * 32];
-                pos[i] = spos[i0 + i * 32];
+                const uint2 v = entries[i0 + i * 32];
+                key[i] = v.x;
+                pos[i] = v.y;
             }
-    }
-    for (uint32_t at = threadIdx.x; at < tokens; at += kSortThreads) {
-        keys_out[at] = skeys[at];
-        pos_out[at] = spos[at];
     }
 }
 
@@ -448,6 +542,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 
 struct GradParams {
     const uint32_t *keys, *pos, *nvalid;
+    uint32_t tokens;       // entries that keys and pos have room for
     uint32_t range;        // sorted entries per range, before its ends move to the ends of runs
     uint32_t units;        // per row
     float scale;
@@ -503,20 +598,50 @@ __device__ __forceinline__ uint32_t range_begin(const uint32_t *keys, uint32_t n
 
 // LPR lanes per range and V columns per lane. A range adds up the rows of its runs of equal keys
 // one after the other in fp32; a whole run goes to its table row, a cut one to the range's slots,
-// and the range that a cut run begins in enters the run into the list of joins.
-template <typename T, typename O, int V, int LPR>
+// and the range that a cut run begins in enters the run into the list of joins. SHORT: a range's
+// possible entries are at most LPR, read in one go together with the search for its ends.
+template <typename T, typename O, int V, int LPR, bool SHORT>
 __global__ void __launch_bounds__(kGradThreads)
     grad_ranges_kernel(const T *__restrict__ dY, const GradParams p, O *__restrict__ dC) {
     constexpr int GROUPS = kGradThreads / LPR;
-    constexpr int U = LPR < 8 ? LPR : (V * sizeof(T) >= 16 ? 4 : 8);   // rows in flight per group
+    constexpr int U = LPR < 8 ? LPR : (V * sizeof(T) >= 16 && !SHORT ? 4 : 8);   // rows in flight per group
     const int t = threadIdx.x % LPR;
-    const uint32_t n = *p.nvalid;
     const uint32_t r = blockIdx.x * static_cast<uint32_t>(GROUPS) + threadIdx.x / LPR;
     const uint64_t first = static_cast<uint64_t>(r) * p.range;
+    uint32_t key0 = 0, pos0 = 0, before = 0;
+    if (SHORT) {      // read ahead of the number of entries: the arrays hold a value for every token
+        const uint64_t i = first + t;
+        if (i < p.tokens) {
+            key0 = p.keys[i];
+            pos0 = p.pos[i];
+            if (t == 0 && i > 0) before = p.keys[i - 1];
+        }
+    }
+    const uint32_t n = *p.nvalid;
     bool cut0, cut1;
-    const uint32_t s = range_begin<LPR>(p.keys, n, first, p.range, cut0);
-    const uint32_t e = range_begin<LPR>(p.keys, n, first + p.range, p.range, cut1);
-    const uint32_t len = e - s;                     // at most two ranges' entries
+    uint32_t s, len;
+    if (SHORT) {
+        const uint64_t i = first + t;
+        uint32_t prev = __shfl_up_sync(0xffffffffu, key0, 1, LPR);
+        if (t == 0) prev = before;
+        const bool start = i >= n || i == 0 || key0 != prev;
+        uint32_t m = __ballot_sync(0xffffffffu, start);
+        if (LPR < 32) m = (m >> ((threadIdx.x & 31) / LPR * LPR)) & ((1u << (LPR & 31)) - 1);
+        const uint32_t low = (1u << p.range) - 1;         // range <= LPR / 2 <= 16
+        const uint32_t m0 = m & low, m1 = (m >> p.range) & low;
+        const uint32_t left = first >= n ? 0 : static_cast<uint32_t>(min(static_cast<uint64_t>(n) - first, static_cast<uint64_t>(LPR)));
+        const uint32_t so = min(left, m0 ? __ffs(m0) - 1u : 0u), eo = min(left, p.range + (m1 ? __ffs(m1) - 1u : 0u));
+        cut0 = m0 == 0;
+        cut1 = m1 == 0;
+        // entries [so, eo) of the lanes' move to the front
+        key0 = __shfl_sync(0xffffffffu, key0, (t + so) & (LPR - 1), LPR);
+        pos0 = __shfl_sync(0xffffffffu, pos0, (t + so) & (LPR - 1), LPR);
+        s = static_cast<uint32_t>(first) + so;
+        len = eo - so;
+    } else {
+        s = range_begin<LPR>(p.keys, n, first, p.range, cut0);
+        len = range_begin<LPR>(p.keys, n, first + p.range, p.range, cut1) - s;   // at most two ranges' entries
+    }
     const uint32_t c = blockIdx.y * LPR + t;
     const bool in = c < p.units;
     const int64_t d = static_cast<int64_t>(p.units) * V;
@@ -538,7 +663,11 @@ __global__ void __launch_bounds__(kGradThreads)
     };
     for (uint32_t b = 0; __any_sync(0xffffffffu, b < len); b += LPR) {
         const bool have = b + t < len;
-        const uint32_t key = have ? p.keys[s + b + t] : 0, pos = have ? p.pos[s + b + t] : 0;
+        uint32_t key = key0, pos = pos0;
+        if (!SHORT) {
+            key = have ? p.keys[s + b + t] : 0;
+            pos = have ? p.pos[s + b + t] : 0;
+        }
         if (b == 0) cur = __shfl_sync(0xffffffffu, key, 0, LPR);
 #pragma unroll 1
         for (int u0 = 0; u0 < LPR; u0 += U) {
@@ -611,7 +740,7 @@ __global__ void __launch_bounds__(kGradThreads)
         if (in) {
             const uint32_t a = min(count, w * per), e = min(count, a + per);
             const float *slot = p.slots + static_cast<int64_t>(c) * V;
-#pragma unroll 4
+#pragma unroll 8
             for (uint32_t j = a; j < e; ++j) {
                 const float *q = slot + (static_cast<int64_t>(r0 + j) * 2 + (j == 0 ? 1 : 0)) * d;
 #pragma unroll
@@ -716,7 +845,7 @@ km_status lookup_typed(const void *Cv, const int32_t *ids, int64_t B, int64_t N,
 
 // How the tokens of a call are sorted.
 struct SortPlan {
-    bool small;              // one block, in shared memory
+    bool small;              // one cluster, in shared memory
     int64_t segs, n, tps;    // otherwise: segments, their tokens, tiles per segment
     bool by_batch;
     int passes, width;       // digits
@@ -795,11 +924,13 @@ km_status grad_sort(const int32_t *ids, int64_t B, int64_t N, int64_t K, const G
     s.width = p.width;
     if (p.small) {
         if (cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kSortSmem)) != cudaSuccess)
+                                 static_cast<int>(kSmallSmem)) != cudaSuccess)
             return KM_ERR_CUDA;
-        // a zeroing block per 64 KB, one per SM at most
-        const int64_t fill = zero ? std::min<int64_t>(std::max(1, num_sms() - 1), ceil_div(static_cast<int64_t>(zero_bytes), 65536)) : 0;
-        sort_small_kernel<<<static_cast<unsigned>(1 + fill), kSortThreads, kSortSmem, st>>>(
+        s.divE = make_fastdiv(static_cast<uint32_t>(ceil_div(T, kCluster * kSortThreads) * kSortThreads));
+        // a zeroing block per 64 KB, one per SM at most (whole clusters)
+        const int64_t blocks = zero ? std::min<int64_t>(std::max(0, num_sms() - kCluster), ceil_div(static_cast<int64_t>(zero_bytes), 65536)) : 0;
+        const int64_t fill = zero ? std::max<int64_t>(1, blocks / kCluster) * kCluster : 0;
+        sort_small_kernel<<<static_cast<unsigned>(kCluster + fill), kSortThreads, kSmallSmem, st>>>(
             s, static_cast<uint32_t>(T), static_cast<uint32_t>(B * K), p.passes, w.keys[0], w.pos[0], w.segstart, w.jobs,
             static_cast<uint8_t *>(zero), zero_bytes);
         *side = 0;
@@ -847,7 +978,13 @@ template <typename T, typename O, int V, int LPR>
 km_status grad_sum(const T *dY, const GradParams &p, int64_t ranges, O *dC, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>(ceil_div(ranges, kGradThreads / LPR)), static_cast<unsigned>(ceil_div(p.units, LPR)));
     if (grid.y > kMaxGridY) return KM_ERR_UNSUPPORTED;   // never: d <= 2^20 and 32 lanes per block
-    grad_ranges_kernel<T, O, V, LPR><<<grid, kGradThreads, 0, st>>>(dY, p, dC);
+    bool launched = false;
+    if constexpr (LPR >= 32)
+        if (2 * p.range <= LPR) {
+            grad_ranges_kernel<T, O, V, LPR, true><<<grid, kGradThreads, 0, st>>>(dY, p, dC);
+            launched = true;
+        }
+    if (!launched) grad_ranges_kernel<T, O, V, LPR, false><<<grid, kGradThreads, 0, st>>>(dY, p, dC);
     if (launch_status() != KM_OK) return KM_ERR_CUDA;
     if (ranges > 1) {
         const unsigned cols = static_cast<unsigned>(ceil_div(p.units, 32));
@@ -924,6 +1061,7 @@ km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int
     if (s != KM_OK) return s;
     p.keys = w.keys[side];
     p.pos = w.pos[side];
+    p.tokens = static_cast<uint32_t>(B * N);
     p.range = static_cast<uint32_t>(grad_range(B * N));
     p.scale = scale;
     p.accumulate = accumulate ? 1 : 0;

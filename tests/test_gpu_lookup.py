@@ -88,7 +88,9 @@ def test_lookup_grad(cuda_device, dtype, out, B, N, K, d):
 
 
 @pytest.mark.parametrize("B,N,K,d", [(1, 5000, 7, 8), (1, 40000, 3, 32), (2, 9000, 70000, 4), (1, 70000, 300000, 1),
-                                     (1, 300000, 20, 16), (3, 4096, 1, 64), (1, 4097, 256, 64), (1, 4096, 257, 20)])
+                                     (1, 300000, 20, 16), (3, 4096, 1, 64), (1, 4097, 256, 64), (1, 4096, 257, 20),
+                                     (1, 65536, 1024, 8), (1, 65537, 1025, 8), (5, 16484, 1200, 8), (3, 30000, 5000, 4),
+                                     (100, 1000, 50, 8), (1, 600000, 300, 2), (2, 540000, 3000, 1), (9, 8192, 1024, 16)])
 @pytest.mark.parametrize("kind", ["random", "skewed", "holes", "one"])
 def test_lookup_grad_large_sorts(cuda_device, B, N, K, d, kind):
     # several sort tiles and passes, runs over many ranges; small integers, so every sum is exact
