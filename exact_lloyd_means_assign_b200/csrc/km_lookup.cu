@@ -394,7 +394,15 @@ __device__ __forceinline__ void zero_fill(uint8_t *p, size_t bytes, size_t i, si
     if (i < head) p[i] = 0;
     uint4 *v = reinterpret_cast<uint4 *>(p + head);
     const size_t units = (bytes - head) / 16;
-    for (size_t u = i; u < units; u += threads) v[u] = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    size_t u = i;
+    for (; u + 3 * threads < units; u += 4 * threads) {
+        v[u] = z;
+        v[u + threads] = z;
+        v[u + 2 * threads] = z;
+        v[u + 3 * threads] = z;
+    }
+    for (; u < units; u += threads) v[u] = z;
     const size_t tail = head + units * 16;
     if (tail + i < bytes) p[tail + i] = 0;
 }
@@ -567,6 +575,27 @@ __device__ __forceinline__ void write_row(O *out, const float (&acc)[V], float s
     }
 }
 
+// V fp32 values of a slot, in 16-byte accesses where V allows.
+template <int V> __device__ __forceinline__ void store_slot(float *p, const float (&v)[V]) {
+    constexpr int W = V < 4 ? V : 4;
+#pragma unroll
+    for (int h = 0; h < V; h += W) {
+        Vec<float, W> o;
+#pragma unroll
+        for (int i = 0; i < W; ++i) o.v[i] = v[h + i];
+        *reinterpret_cast<Vec<float, W> *>(p + h) = o;
+    }
+}
+template <int V> __device__ __forceinline__ void add_slot(const float *p, float (&v)[V]) {
+    constexpr int W = V < 4 ? V : 4;
+#pragma unroll
+    for (int h = 0; h < V; h += W) {
+        const Vec<float, W> o = *reinterpret_cast<const Vec<float, W> *>(p + h);
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[h + i] += o.v[i];
+    }
+}
+
 constexpr int kGradThreads = 256;
 
 // Where range r begins: the first start of a run in [r L, (r + 1) L), so that a run is summed by
@@ -655,8 +684,7 @@ __global__ void __launch_bounds__(kGradThreads)
         if (!in) return;
         if (head || tail) {
             float *slot = p.slots + (static_cast<int64_t>(r) * 2 + (head ? 0 : 1)) * d + static_cast<int64_t>(c) * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) slot[i] = acc[i];
+            store_slot<V>(slot, acc);
         } else {
             write_row<O, V>(dC + static_cast<int64_t>(cur) * d + static_cast<int64_t>(c) * V, acc, p.scale, p.accumulate);
         }
@@ -742,9 +770,7 @@ __global__ void __launch_bounds__(kGradThreads)
             const float *slot = p.slots + static_cast<int64_t>(c) * V;
 #pragma unroll 8
             for (uint32_t j = a; j < e; ++j) {
-                const float *q = slot + (static_cast<int64_t>(r0 + j) * 2 + (j == 0 ? 1 : 0)) * d;
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += q[i];
+                add_slot<V>(slot + (static_cast<int64_t>(r0 + j) * 2 + (j == 0 ? 1 : 0)) * d, acc);
             }
         }
 #pragma unroll
@@ -927,9 +953,31 @@ km_status grad_sort(const int32_t *ids, int64_t B, int64_t N, int64_t K, const G
                                  static_cast<int>(kSmallSmem)) != cudaSuccess)
             return KM_ERR_CUDA;
         s.divE = make_fastdiv(static_cast<uint32_t>(ceil_div(T, kCluster * kSortThreads) * kSortThreads));
-        // a zeroing block per 64 KB, one per SM at most (whole clusters)
-        const int64_t blocks = zero ? std::min<int64_t>(std::max(0, num_sms() - kCluster), ceil_div(static_cast<int64_t>(zero_bytes), 65536)) : 0;
-        const int64_t fill = zero ? std::max<int64_t>(1, blocks / kCluster) * kCluster : 0;
+        // A zeroing block per 64 KB, but no more clusters than can be resident beside the sorting one:
+        // a second wave would double the time.
+        static int resident[64] = {0};
+        int dev = 0;
+        cudaGetDevice(&dev);
+        int clusters = (dev >= 0 && dev < 64) ? resident[dev] : 0;
+        if (clusters <= 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(kCluster * 16);
+            cfg.blockDim = dim3(kSortThreads);
+            cfg.dynamicSmemBytes = kSmallSmem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = kCluster;
+            attr.val.clusterDim.y = 1;
+            attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&clusters, sort_small_kernel, &cfg) != cudaSuccess || clusters <= 1) {
+                cudaGetLastError();
+                clusters = 2;
+            }
+            if (dev >= 0 && dev < 64) resident[dev] = clusters;
+        }
+        const int64_t fill = zero ? std::min<int64_t>(clusters - 1, std::max<int64_t>(1, ceil_div(static_cast<int64_t>(zero_bytes), 65536 * kCluster))) * kCluster : 0;
         sort_small_kernel<<<static_cast<unsigned>(kCluster + fill), kSortThreads, kSmallSmem, st>>>(
             s, static_cast<uint32_t>(T), static_cast<uint32_t>(B * K), p.passes, w.keys[0], w.pos[0], w.segstart, w.jobs,
             static_cast<uint8_t *>(zero), zero_bytes);
