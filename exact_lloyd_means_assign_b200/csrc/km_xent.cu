@@ -10,7 +10,10 @@ namespace {
 
 using namespace km::xe;
 
-constexpr int64_t kPieceElems = int64_t{1} << 27;   // entries of P held at a time (256 MiB of 16-bit)
+// Entries of P held at a time (256 MiB of 16-bit). Pieces that stay in L2 lose more to short launches
+// than they save in traffic (8192 x 32768 points x rows at d = 1024, forward and backward: 2^25
+// entries 1.77 ms, 2^26 1.60, 2^27 1.57).
+constexpr int64_t kPieceElems = int64_t{1} << 27;
 constexpr int kPieceStep = 256;
 
 inline bool xent_sizes_ok(int64_t B, int64_t N, int64_t K, int64_t d) {
@@ -40,8 +43,9 @@ inline int64_t product_splits(int64_t B, int64_t M, int64_t N, int64_t Kk, km_dt
 // fp16 and bf16 run on the tensor cores. Rows that are no multiple of 16 bytes are copied to padded
 // ones first; rows that are, but in a buffer that does not start on 16 bytes, take the CUDA cores.
 inline int64_t padded(int64_t d, km_dtype dt) { return dt == KM_F32 ? d : ceil_div(d, 8) * 8; }
-inline bool use_tc(km_dtype dt, int64_t d, const void *X, const void *C) {
-    return dt != KM_F32 && (d % 8 != 0 || (aligned(X, 16) && aligned(C, 16))) && encode_fn() != nullptr;
+// (A scale of zero takes them too: the tensor-core epilogue keeps its maximum before the scaling.)
+inline bool use_tc(km_dtype dt, int64_t d, float scale, const void *X, const void *C) {
+    return dt != KM_F32 && scale != 0.f && (d % 8 != 0 || (aligned(X, 16) && aligned(C, 16))) && encode_fn() != nullptr;
 }
 
 struct LossWs {
@@ -119,12 +123,22 @@ inline bool encode_operand(CUtensorMap *tm, CUtensorMapDataType tdt, const Opera
 template <typename T, int BN, int MODE, bool AMN, bool BMN>
 km_status tc_launch(const Operand &A, const Operand &Bo, int64_t B, int64_t M, int64_t N, int64_t Kk, Epi e,
                     int64_t splits, cudaStream_t st) {
-    using Sh = TcShape<BN>;
+    using Sh = TcShape<BN, MODE>;
     const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     const CUtensorMapDataType tdt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap tmA, tmB;
     if (!encode_operand(&tmA, tdt, A, M, Kk, B, TBM) || !encode_operand(&tmB, tdt, Bo, N, Kk, B, BN / 2))
         return KM_ERR_CUDA;
+    CUtensorMap tmP = tmA;      // (read where P is written only)
+    if (MODE == kProb) {
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(e.ldp), static_cast<cuuint64_t>(M), static_cast<cuuint64_t>(B)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(e.ldp * 2), static_cast<cuuint64_t>(M * e.ldp * 2)};
+        const cuuint32_t box[3] = {64, 32, 1}, estr[3] = {1, 1, 1};
+        if (encode_fn()(&tmP, tdt, 3, e.P, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return KM_ERR_CUDA;
+    }
     auto kernel = tc_product_kernel<T, BN, MODE, AMN, BMN>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Sh::kTotal)) !=
         cudaSuccess)
@@ -161,13 +175,14 @@ km_status tc_launch(const Operand &A, const Operand &Bo, int64_t B, int64_t M, i
     p.Kk = static_cast<int>(Kk);
     p.kchunks = static_cast<int>(ceil_div(Kk, TKC));
     p.kper = static_cast<int>(ceil_div(p.kchunks, splits));
-    p.idesc = km::mma_idesc_f16(bf16 ? 1u : 0u, 2 * TBM, BN) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+    p.idesc = km::mma_idesc_f16(bf16 ? 1u : 0u, 2 * TBM, BN) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
+              (MODE != kOut && e.scale < 0.f ? 1u << 13 : 0u);   // bit 13 negates A
     p.vec = N % 8 == 0 && (!e.outT || aligned(e.outT, 16)) ? 1 : 0;
     e.splits = static_cast<int>(splits);
     const int64_t items = static_cast<int64_t>(p.mt) * p.nt * splits * B;
     if (items > kMaxIndex) return KM_ERR_UNSUPPORTED;
     const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(items, clusters));
-    kernel<<<grid, T_THREADS, Sh::kTotal, st>>>(tmA, tmB, p, e);
+    kernel<<<grid, T_THREADS, Sh::kTotal, st>>>(tmA, tmB, tmP, p, e);
     return launch_status();
 }
 
@@ -213,16 +228,22 @@ km_status out_product(bool tc, km_dtype dt, const Operand &A, const Operand &Bo,
 template <typename T>
 km_status copy_rows(const void *src, const int32_t *ids, int64_t rows, int64_t d, int64_t dp, int64_t K, void *dst,
                     cudaStream_t st) {
-    copy_rows_kernel<T><<<fill_blocks(rows * dp), 256, 0, st>>>(static_cast<const T *>(src), ids, rows,
-                                                                static_cast<int>(d), static_cast<int>(dp),
-                                                                static_cast<int>(K), static_cast<T *>(dst));
+    const int64_t v = 16 / sizeof(T);
+    if (d == dp && d % v == 0 && aligned(src, 16) && aligned(dst, 16))
+        copy_rows_kernel<uint4><<<fill_blocks(rows * d / v), 256, 0, st>>>(
+            static_cast<const uint4 *>(src), ids, rows, static_cast<int>(d / v),
+            km::make_fastdiv(static_cast<uint32_t>(d / v)), static_cast<int>(K), static_cast<uint4 *>(dst));
+    else
+        copy_rows_kernel<T><<<fill_blocks(rows * dp), 256, 0, st>>>(
+            static_cast<const T *>(src), ids, rows, static_cast<int>(d), km::make_fastdiv(static_cast<uint32_t>(dp)),
+            static_cast<int>(K), static_cast<T *>(dst));
     return launch_status();
 }
 
 template <typename T>
 km_status loss_typed(const void *X, km_dtype dt, const void *C, const int32_t *ids, int64_t B, int64_t N, int64_t K,
                      int64_t d, float scale, float *loss, float *lse, const LossWs &w, cudaStream_t st) {
-    const bool tc = use_tc(dt, d, X, C);
+    const bool tc = use_tc(dt, d, scale, X, C);
     const int64_t dp = tc ? padded(d, dt) : d;
     km_status s;
     if (dp != d) {
@@ -250,7 +271,7 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
                      cudaStream_t st) {
     Carver cv(ws);
     const GradWs w = carve_grad(cv, B, N, K, d, dt);
-    const bool tc = use_tc(dt, d, X, C);
+    const bool tc = use_tc(dt, d, scale, X, C);
     const int64_t dp = tc ? padded(d, dt) : d;
     km_status s;
     unsigned int *wmax = dt == KM_F16 ? w.wmax : nullptr;

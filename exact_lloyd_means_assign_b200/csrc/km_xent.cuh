@@ -186,35 +186,39 @@ __global__ void __launch_bounds__(kSimtThreads)
 
 // ------------------------------------------------------------------ small kernels around them
 
-// loss and lse from the per-tile pairs: 32 rows x 8 slices of the tiles per block, slices and
-// tiles joined in a fixed order.
+// loss and lse from the per-tile pairs: 32 rows x 8 slices of the tiles per block. The row's maximum
+// first, then the sums against it; slices and tiles are joined in a fixed order.
 __global__ void __launch_bounds__(256)
     lse_join_kernel(const float2 *__restrict__ pairs, const float *__restrict__ zt, const int32_t *__restrict__ ids,
                     int64_t B, int N, int K, int tiles, float *__restrict__ loss, float *__restrict__ lse) {
-    __shared__ float sm[8][32], ss[8][32];
+    __shared__ float part[8][32];
     const int x = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int64_t per = (N + 31) / 32;
     const int64_t b = blockIdx.x / per;
     const int row = static_cast<int>(blockIdx.x % per) * 32 + x;
+    const bool in = row < N;
     const float2 *pr = pairs + b * tiles * N + row;
-    float m = -INFINITY, s = 0.f;
-    if (row < N)
+    float m = -INFINITY;
+    if (in)
+#pragma unroll 8
+        for (int t = q; t < tiles; t += 8) m = fmaxf(m, pr[static_cast<int64_t>(t) * N].x);
+    part[q][x] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i][x]);
+    __syncthreads();
+    float s = 0.f;
+    if (in)
+#pragma unroll 8
         for (int t = q; t < tiles; t += 8) {
             const float2 v = pr[static_cast<int64_t>(t) * N];
-            const float mm = fmaxf(m, v.x);
-            s = s * expf(m - mm) + v.y * expf(v.x - mm);
-            m = mm;
+            s = fmaf(v.y, expf(v.x - m), s);
         }
-    sm[q][x] = m;
-    ss[q][x] = s;
+    part[q][x] = s;
     __syncthreads();
-    if (q == 0 && row < N) {
-        for (int i = 1; i < 8; ++i)
-            if (i < tiles) {
-                const float mm = fmaxf(m, sm[i][x]);
-                s = s * expf(m - mm) + ss[i][x] * expf(sm[i][x] - mm);
-                m = mm;
-            }
+    if (q == 0 && in) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += part[i][x];
         const float l = m + logf(s);
         const int64_t at = b * N + row;
         const int id = ids[at];
@@ -243,20 +247,27 @@ __global__ void __launch_bounds__(256)
 
 // Rows of src [rows, d] to dst [rows, dp] (dp >= d, the rest zeros); with ids, rows without a
 // label become zeros, so that whatever they hold cannot reach a sum over rows.
-template <typename T>
+// U is the unit of copying: T, or uint4 where rows are whole 16-byte units and dp == d (both counted
+// in units).
+template <typename U>
 __global__ void __launch_bounds__(256)
-    copy_rows_kernel(const T *__restrict__ src, const int32_t *__restrict__ ids, int64_t rows, int d, int dp, int K,
-                     T *__restrict__ dst) {
-    const int64_t total = rows * dp;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const int64_t r = i / dp;
-        const int c = static_cast<int>(i - r * dp);
-        bool keep = c < d;
-        if (ids && keep) {
-            const int id = ids[r];
-            keep = id >= 0 && id < K;
+    copy_rows_kernel(const U *__restrict__ src, const int32_t *__restrict__ ids, int64_t rows, int d, FastDiv dp, int K,
+                     U *__restrict__ dst) {
+    // rows in slices whose units number less than 2^31
+    const int64_t slice = ((int64_t{1} << 31) - 1) / dp.d;
+    for (int64_t r0 = 0; r0 < rows; r0 += slice) {
+        const uint32_t total = static_cast<uint32_t>(min(slice, rows - r0)) * dp.d;
+        for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < total; i += gridDim.x * 256ull) {
+            const uint32_t r = fd_div(dp, static_cast<uint32_t>(i)), c = static_cast<uint32_t>(i) - r * dp.d;
+            bool keep = c < static_cast<uint32_t>(d);
+            if (ids && keep) {
+                const int id = ids[r0 + r];
+                keep = id >= 0 && id < K;
+            }
+            U v = {};
+            if (keep) v = src[(r0 + r) * d + c];
+            dst[r0 * dp.d + i] = v;
         }
-        dst[i] = keep ? src[r * d + c] : Cvt<T>::from_f(0.f);
     }
 }
 

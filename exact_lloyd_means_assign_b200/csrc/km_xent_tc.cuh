@@ -31,13 +31,17 @@ constexpr int TBM = 128;                 // rows per CTA, 256 per pair
 constexpr int TKC = 64;                  // reduction steps per stage (128 bytes of 16-bit values)
 constexpr int T_EPI0 = 4, T_EPI_WARPS = 8;
 constexpr int T_THREADS = 32 * (T_EPI0 + T_EPI_WARPS);
+constexpr uint32_t kOutBuf = 32 * 128;    // bytes of a P store
 constexpr int T_GROUP = 8;               // row tiles that share their column tiles in L2
 
-template <int BN> struct TcShape {
+template <int BN, int MODE> struct TcShape {
     static constexpr uint32_t kA = TBM * 128u, kB = (BN / 2) * 128u;
     static constexpr uint32_t kStage = kA + kB;
-    static constexpr int kStages = BN == 256 ? 6 : 8;
-    static constexpr uint32_t kBarOff = kStages * kStage;
+    // kProb: two 32-row x 64-column buffers per epilogue warp, from which P is stored by TMA
+    static constexpr uint32_t kOutBytes = MODE == kProb ? T_EPI_WARPS * 2 * kOutBuf : 0;
+    static constexpr int kStages = BN == 256 ? (MODE == kProb ? 5 : 6) : 8;
+    static constexpr uint32_t kOutOff = kStages * kStage;
+    static constexpr uint32_t kBarOff = kOutOff + kOutBytes;
     static constexpr int kBars = 2 * kStages + 5;
     static constexpr uint32_t kTotal = kBarOff + kBars * 8 + 16 + 1024;
 };
@@ -70,6 +74,30 @@ __device__ __forceinline__ TcItem tc_item(const TcParams &p, int splits, int t) 
     return it;
 }
 
+// Two fp32 values in one register pair, for the packed fp32 arithmetic of sm_100.
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair_f32(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ float ex2f(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -98,8 +126,8 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, f
 template <typename T, int BN, int MODE, bool AMN, bool BMN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
     tc_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const TcParams p, const Epi ep) {
-    using Sh = TcShape<BN>;
+                      const __grid_constant__ CUtensorMap tmP, const TcParams p, const Epi ep) {
+    using Sh = TcShape<BN, MODE>;
     using namespace km::tc;
     constexpr int S = Sh::kStages;
     constexpr int HALF = BN / 2;             // columns per epilogue warp
@@ -234,88 +262,138 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
         const int q = warp & 3, half = (warp - T_EPI0) >> 2;
         const uint32_t empty0 = map_to_rank(ACC_EMPTY(0), 0), empty1 = map_to_rank(ACC_EMPTY(1), 0);
         const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * HALF;
-        const float s2 = ep.scale * kLog2e;
+        // The products are formed with |scale| (a negative scale negates the points in the MMA).
+        const float sc = fabsf(ep.scale), s2 = sc * kLog2e;
+        const uint64_t s22 = pair_f32(s2, s2);
         const float fac = MODE == kProb ? pow2_factor(ep.wmax, false) : 1.f;
         const float inv = MODE == kOut && ep.splits == 1 ? pow2_factor(ep.wmax, true) : 1.f;
-        int buf = 0;
+        const uint32_t obuf = sbase + Sh::kOutOff + (warp - T_EPI0) * 2 * kOutBuf;
+        int buf = 0, ob = 0;
         uint32_t aph = 0;
         for (int t = t0; t < total; t += tstep) {
             const TcItem it = tc_item(p, ep.splits, t);
-            const int row = it.m * (2 * TBM) + static_cast<int>(rank) * TBM + q * 32 + lane;
+            const int row0 = it.m * (2 * TBM) + static_cast<int>(rank) * TBM + q * 32, row = row0 + lane;
             const int c0 = it.n * BN + half * HALF;
             const bool rin = row < p.M;
             const int64_t br = static_cast<int64_t>(it.b) * p.M + row;
             int label = -1;
-            float w = 0.f, lse2 = 0.f;
-            bool has = false;
+            // kProb: P = sign (2^(z log2e + off) - |w| [label]) with off = log2 |w| - lse log2e
+            float aw = 0.f, off = 0.f;
+            uint32_t sign = 0, keep = 0;
             if (MODE != kOut && rin) {
                 label = ep.ids[br];
-                has = label >= 0 && label < ep.K;
+                const bool has = label >= 0 && label < ep.K;
                 label = has ? label - ep.k0 : -1;
                 if (MODE == kProb) {
-                    w = ep.w[br] * fac;
-                    lse2 = ep.lse[br] * kLog2e;
+                    const float w = ep.w[br] * fac;
+                    aw = fabsf(w);
+                    off = __log2f(aw) - ep.lse[br] * kLog2e;
+                    sign = w < 0.f ? 0x80008000u : 0u;
+                    keep = has ? ~0u : 0u;
                 }
             }
             if (!mbar_wait_warp(ACC_FULL(buf), aph, abortp)) break;
             tc_fence_after();
-            float m = -INFINITY, s = 0.f;
-#pragma unroll 1
-            for (int c = 0; c < HALF; c += 32) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tl + buf * ACC_STRIDE + c, v);
+            float m = 0.f;
+            uint64_t s4[4] = {0, 0, 0, 0};
+            // columns in chunks of 32, the next chunk's load in flight while one is worked on
+            uint32_t v2[2][32];
+            tmem_ld_32x32b_x32(tl + buf * ACC_STRIDE, v2[0]);
+#pragma unroll
+            for (int ch = 0; ch < HALF / 32; ++ch) {
+                uint32_t(&v)[32] = v2[ch & 1];
                 tmem_wait_ld(v);
-                if (c + 32 == HALF) {
+                if (ch + 1 < HALF / 32) {
+                    tmem_ld_32x32b_x32(tl + buf * ACC_STRIDE + (ch + 1) * 32, v2[(ch + 1) & 1]);
+                } else {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(buf ? empty1 : empty0);
                 }
-                const int col = c0 + c;
+                const int col = c0 + ch * 32;
                 if (MODE == kLse) {
-                    if (col >= p.N) continue;
-                    float z[32];
+                    if (col < p.N) {
+                        if (col + 32 > p.N) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        z[i] = __uint_as_float(v[i]) * s2;
-                        if (col + i >= p.N) z[i] = -INFINITY;
-                    }
-                    float cm = z[0];
+                            for (int i = 0; i < 32; ++i)
+                                if (col + i >= p.N) v[i] = 0xff800000u;      // -inf
+                        }
+                        float cm = __uint_as_float(v[0]), cm2 = __uint_as_float(v[1]);
 #pragma unroll
-                    for (int i = 1; i < 32; ++i) cm = fmaxf(cm, z[i]);
-                    const float nm = fmaxf(m, cm);
-                    s *= ex2f(m - nm);
-                    m = nm;
-                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                        for (int i = 2; i < 30; i += 4) {
+                            cm = max3f(cm, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                            cm2 = max3f(cm2, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+                        }
+                        cm = max3f(max3f(cm, __uint_as_float(v[30]), __uint_as_float(v[31])), cm2, cm);
+                        const float nm = ch ? fmaxf(m, cm) : cm;
+                        if (ch) {
+                            const float corr = ex2f((m - nm) * s2);
+                            const uint64_t c2 = pair_f32(corr, corr);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s4[i & 3] += ex2f(z[i] - m);
-                    s += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                    if (label >= col && label < col + 32) {
-                        float zt = 0.f;
+                            for (int i = 0; i < 4; ++i) s4[i] = fma2(s4[i], c2, 0ull);
+                        }
+                        m = nm;
+                        const float d = -nm * s2;
+                        const uint64_t d2 = pair_f32(d, d);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (col + i == label) zt = __uint_as_float(v[i]) * ep.scale;
-                        ep.zt[br] = zt;
+                        for (int i = 0; i < 32; i += 2) {
+                            float a, b;
+                            unpair_f32(fma2(pair_f32(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s22, d2), a, b);
+                            s4[(i >> 1) & 3] = add2(s4[(i >> 1) & 3], pair_f32(ex2f(a), ex2f(b)));
+                        }
+                        if (label >= col && label < col + 32) {
+                            float zt = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (col + i == label) zt = __uint_as_float(v[i]) * sc;
+                            ep.zt[br] = zt;
+                        }
                     }
                 } else if (MODE == kProb) {
-                    float q32[32];
+                    const uint64_t o2 = pair_f32(off, off);
+                    uint32_t o[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) q32[i] = w * ex2f(fmaf(__uint_as_float(v[i]), s2, -lse2));
+                    for (int i = 0; i < 32; i += 2) {
+                        float a, b;
+                        unpair_f32(fma2(pair_f32(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s22, o2), a, b);
+                        o[i >> 1] = (pack2<T>(ex2f(a), ex2f(b)) ^ sign) & keep;
+                    }
                     if (label >= col && label < col + 32) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (col + i == label) q32[i] = w * (ex2f(fmaf(__uint_as_float(v[i]), s2, -lse2)) - 1.f);
+                            if (col + i == label) {
+                                const float e = ex2f(fmaf(__uint_as_float(v[i]), s2, off)) - aw;
+                                const uint32_t e16 = (pack2<T>(e, e) ^ sign) & keep;
+                                o[i >> 1] = i & 1 ? __byte_perm(o[i >> 1], e16, 0x7610) : __byte_perm(o[i >> 1], e16, 0x3254);
+                            }
                     }
-                    if (rin) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(ep.P) + br * ep.ldp + col);
+                    // 64 columns (two chunks) per buffer, in the 128-byte swizzle of the store's map
+                    const uint32_t dst = obuf + ob * kOutBuf + lane * 128;
+                    if ((ch & 1) == 0) {
+                        // the buffer's store before last has been read out
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        __syncwarp();
+                    }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint4 o;
-                            o.x = has ? pack2<T>(q32[i * 8], q32[i * 8 + 1]) : 0u;
-                            o.y = has ? pack2<T>(q32[i * 8 + 2], q32[i * 8 + 3]) : 0u;
-                            o.z = has ? pack2<T>(q32[i * 8 + 4], q32[i * 8 + 5]) : 0u;
-                            o.w = has ? pack2<T>(q32[i * 8 + 6], q32[i * 8 + 7]) : 0u;
-                            dst[i] = o;
+                    for (int i = 0; i < 4; ++i)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         dst + ((((ch & 1) * 4 + i) ^ (lane & 7)) * 16)),
+                                     "r"(o[i * 4]), "r"(o[i * 4 + 1]), "r"(o[i * 4 + 2]), "r"(o[i * 4 + 3])
+                                     : "memory");
+                    if (ch & 1) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        // columns behind the piece's last are inside the row's padding or cut off
+                        if (lane == 0) {
+                            if (row0 < p.M && col - 32 < p.N)
+                                asm volatile(
+                                    "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                                        &tmP),
+                                    "r"(obuf + ob * kOutBuf), "r"(col - 32), "r"(row0), "r"(it.b)
+                                    : "memory");
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                         }
+                        ob ^= 1;
                     }
                 } else {
                     if (!rin || col >= p.N) continue;
@@ -381,12 +459,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                 }
             }
             if (MODE == kLse && rin && c0 < p.N) {
-                // pairs are kept in natural units
+                float a, b;
+                unpair_f32(add2(add2(s4[0], s4[1]), add2(s4[2], s4[3])), a, b);
                 const int64_t tiles = (p.N + ST - 1) / ST;
-                ep.pairs[(static_cast<int64_t>(it.b) * tiles + it.n * 2 + half) * p.M + row] = make_float2(m / kLog2e, s);
+                ep.pairs[(static_cast<int64_t>(it.b) * tiles + it.n * 2 + half) * p.M + row] = make_float2(m * sc, a + b);
             }
             buf ^= 1;
             if (buf == 0) aph ^= 1u;
+        }
+        if (MODE == kProb) {      // every store has been read out of shared memory and written
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+            __syncwarp();
         }
     }
     // both CTAs are done with each other's barriers and the leader's MMAs have drained

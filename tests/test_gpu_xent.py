@@ -94,7 +94,7 @@ def _check_grad(X, C, ids, g, scale, dX, dC):
 @pytest.mark.parametrize("B,N,K,d", SHAPES)
 def test_xent_and_gradients(cuda_device, dtype, B, N, K, d):
     X, C, ids, g = _inputs(B, N, K, d, dtype, cuda_device, seed=N + K + d)
-    for scale, gr in ((1.0, g), (0.25, None)):
+    for scale, gr in ((1.0, g), (0.25, None), (-0.5, g), (0.0, g)):
         loss, lse = km.km_xent(X, C, ids, scale)
         dX, dC = km.km_xent_grad(X, C, ids, lse, gr, scale)
         torch.cuda.synchronize()
