@@ -181,6 +181,10 @@ km_status tc_launch(const Operand &A, const Operand &Bo, int64_t B, int64_t M, i
     e.splits = static_cast<int>(splits);
     const int64_t items = static_cast<int64_t>(p.mt) * p.nt * splits * B;
     if (items > kMaxIndex) return KM_ERR_UNSUPPORTED;
+    p.div_split = km::make_fastdiv(static_cast<uint32_t>(p.mt * p.nt));
+    p.div_batch = km::make_fastdiv(static_cast<uint32_t>(p.mt * p.nt * splits));
+    p.div_group = km::make_fastdiv(static_cast<uint32_t>(T_GROUP * p.nt));
+    p.div_last = km::make_fastdiv(static_cast<uint32_t>(p.mt % T_GROUP ? p.mt % T_GROUP : T_GROUP));
     const unsigned grid = static_cast<unsigned>(2 * std::min<int64_t>(items, clusters));
     kernel<<<grid, T_THREADS, Sh::kTotal, st>>>(tmA, tmB, tmP, p, e);
     return launch_status();

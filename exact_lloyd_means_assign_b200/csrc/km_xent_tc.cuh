@@ -16,7 +16,7 @@
 //
 // Roles per CTA (12 warps): warp 0 requests the tiles; warp 1 of the leader issues the MMAs;
 // warps 4-11 are the epilogue (TMEM lane quarter = warp % 4, column half = (warp - 4) / 4, one row
-// per thread). Waits are bounded like everywhere in the library: a role that gives up sets the
+// per thread; sixteen warps with half the columns each were no faster). Waits are bounded like everywhere in the library: a role that gives up sets the
 // CTA's abort flag, the producer waits for the copies it asked for, the issuer for its MMAs, the
 // pair synchronises and frees TMEM. No TMA load uses multicast.
 #pragma once
@@ -54,23 +54,25 @@ struct TcParams {
     int Kk;
     uint32_t idesc;
     int vec;              // rows of the output start on 16-byte boundaries
+    FastDiv div_batch, div_split, div_group, div_last;   // items per batch, per split, per group of
+                                                         // row tiles; row tiles of the last group
 };
 
 struct TcItem {
     int m, n, split, b;
 };
-__device__ __forceinline__ TcItem tc_item(const TcParams &p, int splits, int t) {
+// Work item t: batches, splits, groups of T_GROUP row tiles, columns, row tiles (fastest).
+__device__ __forceinline__ TcItem tc_item(const TcParams &p, int t) {
     TcItem it;
-    const int tiles = p.mt * p.nt, per = tiles * splits;
-    it.b = t / per;
-    int r = t - it.b * per;
-    it.split = r / tiles;
-    r -= it.split * tiles;
-    const int g = r / (T_GROUP * p.nt);
-    r -= g * T_GROUP * p.nt;
-    const int size = min(T_GROUP, p.mt - g * T_GROUP);
-    it.n = r / size;
-    it.m = g * T_GROUP + (r - it.n * size);
+    it.b = fd_div(p.div_batch, t);
+    int r = t - it.b * static_cast<int>(p.div_batch.d);
+    it.split = fd_div(p.div_split, r);
+    r -= it.split * static_cast<int>(p.div_split.d);
+    const int g = fd_div(p.div_group, r);
+    r -= g * static_cast<int>(p.div_group.d);
+    const int left = p.mt - g * T_GROUP;
+    it.n = left >= T_GROUP ? r / T_GROUP : static_cast<int>(fd_div(p.div_last, r));
+    it.m = g * T_GROUP + (r - it.n * min(T_GROUP, left));
     return it;
 }
 
@@ -181,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
         long long uses = 0;
         bool ok = true;
         for (int t = t0; t < total && ok; t += tstep) {
-            const TcItem it = tc_item(p, ep.splits, t);
+            const TcItem it = tc_item(p, t);
             const int mrow = it.m * (2 * TBM) + static_cast<int>(rank) * TBM;
             const int nrow = it.n * BN + static_cast<int>(rank) * (BN / 2);
             const int kc1 = min(p.kchunks, (it.split + 1) * p.kper);
@@ -227,7 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
             uint32_t ph = 0, aph = 0;
             bool ok = true;
             for (int t = t0; t < total && ok; t += tstep) {
-                const TcItem it = tc_item(p, ep.splits, t);
+                const TcItem it = tc_item(p, t);
                 const int kc0 = it.split * p.kper, kc1 = min(p.kchunks, kc0 + p.kper);
                 if (!mbar_wait_warp(ACC_EMPTY(buf), aph ^ 1u, abortp)) break;
                 tc_fence_after();
@@ -270,8 +272,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
         const uint32_t obuf = sbase + Sh::kOutOff + (warp - T_EPI0) * 2 * kOutBuf;
         int buf = 0, ob = 0;
         uint32_t aph = 0;
+        // The row's label, weight and lse, read one tile ahead: their latency would otherwise stand
+        // before every tile's first exponential.
+        int id_n = -1;
+        float w_n = 0.f, lse_n = 0.f;
+        TcItem next = {};
+        auto read_row = [&](int t) {
+            if (t >= total) return;
+            next = tc_item(p, t);
+            if (MODE == kOut) return;
+            const int row = next.m * (2 * TBM) + static_cast<int>(rank) * TBM + q * 32 + lane;
+            id_n = -1;
+            if (row < p.M) {
+                const int64_t br = static_cast<int64_t>(next.b) * p.M + row;
+                id_n = __ldg(ep.ids + br);
+                if (MODE == kProb) {
+                    w_n = __ldg(ep.w + br);
+                    lse_n = __ldg(ep.lse + br);
+                }
+            }
+        };
+        read_row(t0);
         for (int t = t0; t < total; t += tstep) {
-            const TcItem it = tc_item(p, ep.splits, t);
+            const TcItem it = next;
             const int row0 = it.m * (2 * TBM) + static_cast<int>(rank) * TBM + q * 32, row = row0 + lane;
             const int c0 = it.n * BN + half * HALF;
             const bool rin = row < p.M;
@@ -280,18 +303,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
             // kProb: P = sign (2^(z log2e + off) - |w| [label]) with off = log2 |w| - lse log2e
             float aw = 0.f, off = 0.f;
             uint32_t sign = 0, keep = 0;
-            if (MODE != kOut && rin) {
-                label = ep.ids[br];
-                const bool has = label >= 0 && label < ep.K;
-                label = has ? label - ep.k0 : -1;
+            if (MODE != kOut) {
+                const bool has = id_n >= 0 && id_n < ep.K;
+                label = has ? id_n - ep.k0 : -1;
                 if (MODE == kProb) {
-                    const float w = ep.w[br] * fac;
+                    const float w = has ? w_n * fac : 0.f;
                     aw = fabsf(w);
-                    off = __log2f(aw) - ep.lse[br] * kLog2e;
+                    off = __log2f(aw) - lse_n * kLog2e;
                     sign = w < 0.f ? 0x80008000u : 0u;
                     keep = has ? ~0u : 0u;
                 }
             }
+            read_row(t + tstep);
             if (!mbar_wait_warp(ACC_FULL(buf), aph, abortp)) break;
             tc_fence_after();
             float m = 0.f;
@@ -314,6 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                 if (MODE == kLse) {
                     if (col < p.N) {
                         if (col + 32 > p.N) {
+                            asm volatile("");      // a branch: this is the table's last tile only
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (col + i >= p.N) v[i] = 0xff800000u;      // -inf
@@ -342,6 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                             s4[(i >> 1) & 3] = add2(s4[(i >> 1) & 3], pair_f32(ex2f(a), ex2f(b)));
                         }
                         if (label >= col && label < col + 32) {
+                            asm volatile("");
                             float zt = 0.f;
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
@@ -359,6 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                         o[i >> 1] = (pack2<T>(ex2f(a), ex2f(b)) ^ sign) & keep;
                     }
                     if (label >= col && label < col + 32) {
+                        asm volatile("");
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (col + i == label) {
