@@ -421,23 +421,20 @@ def _on_gpu(t, name):
     return dev
 
 
+# The current stream's handle without a Stream object around it, as torch's own launchers read it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _launch_on:
     """Makes `dev` the current device and `stream` (a torch stream, a raw cudaStream_t or None for
     the device's current stream) the current stream, so that outputs and workspaces allocated
-    inside belong to the stream that the kernels run on. The usual call, on the current stream of
-    the current device, changes nothing and enters no context."""
-
-    __slots__ = ("_raw", "_ctx")
+    inside belong to the stream that the kernels run on. Yields the stream's handle."""
 
     def __init__(self, dev, stream):
-        self._ctx = ()
         if stream is None:
             s = torch.cuda.current_stream(dev)
-            self._raw = s.cuda_stream
-            if dev.index != torch.cuda.current_device():
-                self._ctx = (torch.cuda.device(dev),)
-            return
-        if hasattr(stream, "cuda_stream"):
+        elif hasattr(stream, "cuda_stream"):
             s = stream
         elif int(stream) == 0:
             s = torch.cuda.default_stream(dev)
@@ -458,15 +455,24 @@ class _launch_on:
             c.__exit__(*exc)
 
 
+def _launch(dev, stream, call, *args):
+    """call(raw stream, *args) on `dev` and `stream`; the usual call, on the current stream of the
+    current device, enters no context."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(_raw_stream(dev.index), *args)
+    with _launch_on(dev, stream) as s:
+        return call(s, *args)
+
+
 def _a(t):
     """A tensor's address as ctypes takes it for a void pointer (None: null)."""
     return None if t is None else t.data_ptr()
 
 
-def _scratch(ws, nbytes, dev):
+def _scratch(ws, nbytes, like):
     if ws is None:
-        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
-    _need(ws, "ws", torch.uint8, None, dev)
+        return like.new_empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8)
+    _need(ws, "ws", torch.uint8, None, like.device)
     return ws
 
 
@@ -476,12 +482,17 @@ def km_pack4(codes, packed=None, stream=None):
     dev = _on_gpu(codes, "codes")
     _dims(codes, "codes", 2)
     _need(codes, "codes", torch.uint8)
+    return _launch(dev, stream, _pack4, codes, packed)
+
+
+def _pack4(s, codes, packed):
     R, N = codes.shape
-    with _launch_on(dev, stream) as s:
-        shape = (R, 16 * (-(-N // 32)))
-        packed = torch.empty(shape, dtype=torch.uint8, device=dev) if packed is None else packed
-        _need(packed, "packed", torch.uint8, shape, dev)
-        _check("km_pack4", _load().km_pack4(_a(codes), R, N, _a(packed), s))
+    shape = (R, 16 * (-(-N // 32)))
+    if packed is None:
+        packed = codes.new_empty(shape)
+    else:
+        _need(packed, "packed", torch.uint8, shape, codes.device)
+    _check("km_pack4", _load().km_pack4(codes.data_ptr(), R, N, packed.data_ptr(), s))
     return packed
 
 
@@ -492,22 +503,29 @@ def km_matvec4(x, packed, C, scales=None, group=0, y=None, stream=None):
     [R, ceil(N / group)] fp32 with group a multiple of 32, or None. Returns y [M,R] in x's dtype."""
     dev = _on_gpu(x, "x")
     _dims(x, "x", 2)
-    M, N = x.shape
+    N = x.shape[1]
     if C.dim() == 3 and C.shape[2] == 1:
         C = C.view(C.shape[0], C.shape[1])
     _dims(C, "C", 2)
-    R, K = C.shape
+    R = C.shape[0]
     _need(C, "C", torch.float32, None, dev)
     _need(packed, "packed", torch.uint8, (R, 16 * (-(-N // 32))), dev)
     if scales is not None:
         if group < 1:
             raise ValueError("scales need the group size")
         _need(scales, "scales", torch.float32, (R, -(-N // group)), dev)
-    with _launch_on(dev, stream) as s:
-        y = torch.empty((M, R), dtype=x.dtype, device=dev) if y is None else y
-        _need(y, "y", x.dtype, (M, R), dev)
-        _check("km_matvec4", _load().km_matvec4(
-            _a(x), _dt(x.dtype), M, _a(packed), _a(C), R, N, K, _a(scales), group, _a(y), s))
+    return _launch(dev, stream, _matvec4, x, packed, C, scales, group, y)
+
+
+def _matvec4(s, x, packed, C, scales, group, y):
+    (M, N), (R, K) = x.shape, C.shape
+    if y is None:
+        y = x.new_empty((M, R))
+    else:
+        _need(y, "y", x.dtype, (M, R), x.device)
+    _check("km_matvec4", _load().km_matvec4(
+        x.data_ptr(), _dt(x.dtype), M, packed.data_ptr(), C.data_ptr(), R, N, K, _a(scales), group,
+        y.data_ptr(), s))
     return y
 
 
@@ -517,14 +535,19 @@ def km_lookup(C, ids, scale=1.0, Y=None, stream=None):
     dev = _on_gpu(C, "C")
     _dims(C, "C", 3)
     _dims(ids, "ids", 2)
+    _need(ids, "ids", torch.int32, (C.shape[0], ids.shape[1]), dev)
+    return _launch(dev, stream, _lookup, C, ids, scale, Y)
+
+
+def _lookup(s, C, ids, scale, Y):
     B, K, d = C.shape
     N = ids.shape[1]
-    _need(ids, "ids", torch.int32, (B, N), dev)
-    with _launch_on(dev, stream) as s:
-        Y = torch.empty((B, N, d), dtype=C.dtype, device=dev) if Y is None else Y
-        _need(Y, "Y", C.dtype, (B, N, d), dev)
-        _check("km_lookup", _load().km_lookup(
-            _a(C), _dt(C.dtype), _a(ids), B, N, K, d, float(scale), _a(Y), s))
+    if Y is None:
+        Y = C.new_empty((B, N, d))
+    else:
+        _need(Y, "Y", C.dtype, (B, N, d), C.device)
+    _check("km_lookup", _load().km_lookup(
+        C.data_ptr(), _dt(C.dtype), ids.data_ptr(), B, N, K, d, float(scale), Y.data_ptr(), s))
     return Y
 
 
@@ -536,41 +559,61 @@ def km_lookup_grad(dY, ids, K, scale=1.0, dC=None, out_dtype=None, accumulate=Fa
     added to the given dC."""
     dev = _on_gpu(dY, "dY")
     _dims(dY, "dY", 3)
-    B, N, d = dY.shape
-    _need(ids, "ids", torch.int32, (B, N), dev)
+    _need(ids, "ids", torch.int32, dY.shape[:2], dev)
     if accumulate and dC is None:
         raise ValueError("accumulate needs dC")
-    out_dtype = (torch.float32 if dC is None else dC.dtype) if out_dtype is None else out_dtype
-    with _launch_on(dev, stream) as s:
-        dC = torch.empty((B, K, d), dtype=out_dtype, device=dev) if dC is None else dC
-        _need(dC, "dC", out_dtype, (B, K, d), dev)
-        ws = _scratch(ws, _load().km_lookup_grad_workspace_size(B, N, K, d), dev)
-        _check("km_lookup_grad", _load().km_lookup_grad(
-            _a(dY), _dt(dY.dtype), _a(ids), B, N, K, d, float(scale), _a(dC), _dt(out_dtype),
-            int(bool(accumulate)), _a(ws), ws.numel(), s))
+    if out_dtype is None:
+        out_dtype = torch.float32 if dC is None else dC.dtype
+    return _launch(dev, stream, _lookup_grad, dY, ids, K, scale, dC, out_dtype, accumulate, ws)
+
+
+def _lookup_grad(s, dY, ids, K, scale, dC, out_dtype, accumulate, ws):
+    B, N, d = dY.shape
+    if dC is None:
+        dC = dY.new_empty((B, K, d), dtype=out_dtype)
+    else:
+        _need(dC, "dC", out_dtype, (B, K, d), dY.device)
+    lib = _load()
+    ws = _scratch(ws, lib.km_lookup_grad_workspace_size(B, N, K, d), dY)
+    _check("km_lookup_grad", lib.km_lookup_grad(
+        dY.data_ptr(), _dt(dY.dtype), ids.data_ptr(), B, N, K, d, float(scale), dC.data_ptr(),
+        _dt(out_dtype), int(bool(accumulate)), ws.data_ptr(), ws.numel(), s))
     return dC
+
+
+def _xent_args(X, C, ids):
+    dev = _on_gpu(X, "X")
+    _dims(X, "X", 3)
+    _dims(C, "C", 3)
+    B, N, d = X.shape
+    _need(C, "C", X.dtype, (B, C.shape[1], d), dev)
+    _need(ids, "ids", torch.int32, (B, N), dev)
+    return dev
 
 
 def km_xent(X, C, ids, scale=1.0, loss=None, lse=None, ws=None, stream=None):
     """Softmax cross entropy of X [B,N,d] against all rows of C [B,K,d] (same dtype), logits
     scale * <x, c> never stored. ids [B,N] int32; ids outside [0,K) carry no label (loss 0).
     Returns (loss, lse), both [B,N] fp32."""
-    dev = _on_gpu(X, "X")
-    _dims(X, "X", 3)
-    _dims(C, "C", 3)
+    return _launch(_xent_args(X, C, ids), stream, _xent, X, C, ids, scale, loss, lse, ws)
+
+
+def _xent(s, X, C, ids, scale, loss, lse, ws):
     B, N, d = X.shape
     K = C.shape[1]
-    _need(C, "C", X.dtype, (B, K, d), dev)
-    _need(ids, "ids", torch.int32, (B, N), dev)
-    with _launch_on(dev, stream) as s:
-        loss = torch.empty((B, N), dtype=torch.float32, device=dev) if loss is None else loss
-        lse = torch.empty((B, N), dtype=torch.float32, device=dev) if lse is None else lse
-        _need(loss, "loss", torch.float32, (B, N), dev)
-        _need(lse, "lse", torch.float32, (B, N), dev)
-        ws = _scratch(ws, _load().km_xent_workspace_size(B, N, K, d, _dt(X.dtype)), dev)
-        _check("km_xent", _load().km_xent(
-            _a(X), _dt(X.dtype), _a(C), _a(ids), B, N, K, d, float(scale), _a(loss), _a(lse),
-            _a(ws), ws.numel(), s))
+    if loss is None:
+        loss = X.new_empty((B, N), dtype=torch.float32)
+    else:
+        _need(loss, "loss", torch.float32, (B, N), X.device)
+    if lse is None:
+        lse = X.new_empty((B, N), dtype=torch.float32)
+    else:
+        _need(lse, "lse", torch.float32, (B, N), X.device)
+    lib, dt = _load(), _dt(X.dtype)
+    ws = _scratch(ws, lib.km_xent_workspace_size(B, N, K, d, dt), X)
+    _check("km_xent", lib.km_xent(
+        X.data_ptr(), dt, C.data_ptr(), ids.data_ptr(), B, N, K, d, float(scale), loss.data_ptr(),
+        lse.data_ptr(), ws.data_ptr(), ws.numel(), s))
     return loss, lse
 
 
@@ -578,26 +621,28 @@ def km_xent_grad(X, C, ids, lse, g=None, scale=1.0, dX=None, dC=None, want_dX=Tr
                  ws=None, stream=None):
     """Gradients of sum_n g[b,n] * loss[b,n] of km_xent (lse as it returned it; g [B,N] fp32, None =
     ones). Returns (dX [B,N,d], dC [B,K,d]) in X's dtype, None where not wanted."""
-    dev = _on_gpu(X, "X")
-    _dims(X, "X", 3)
-    _dims(C, "C", 3)
+    dev = _xent_args(X, C, ids)
+    _need(lse, "lse", torch.float32, X.shape[:2], dev)
+    _need(g, "g", torch.float32, X.shape[:2], dev)
+    return _launch(dev, stream, _xent_grad, X, C, ids, lse, g, scale, dX, dC, want_dX, want_dC, ws)
+
+
+def _xent_grad(s, X, C, ids, lse, g, scale, dX, dC, want_dX, want_dC, ws):
     B, N, d = X.shape
     K = C.shape[1]
-    _need(C, "C", X.dtype, (B, K, d), dev)
-    _need(ids, "ids", torch.int32, (B, N), dev)
-    _need(lse, "lse", torch.float32, (B, N), dev)
-    _need(g, "g", torch.float32, (B, N), dev)
-    with _launch_on(dev, stream) as s:
-        if want_dX and dX is None:
-            dX = torch.empty((B, N, d), dtype=X.dtype, device=dev)
-        if want_dC and dC is None:
-            dC = torch.empty((B, K, d), dtype=X.dtype, device=dev)
-        _need(dX, "dX", X.dtype, (B, N, d), dev)
-        _need(dC, "dC", X.dtype, (B, K, d), dev)
-        ws = _scratch(ws, _load().km_xent_grad_workspace_size(B, N, K, d, _dt(X.dtype)), dev)
-        _check("km_xent_grad", _load().km_xent_grad(
-            _a(X), _dt(X.dtype), _a(C), _a(ids), _a(lse), _a(g), B, N, K, d, float(scale),
-            _a(dX), _a(dC), _a(ws), ws.numel(), s))
+    if dX is not None:
+        _need(dX, "dX", X.dtype, X.shape, X.device)
+    elif want_dX:
+        dX = torch.empty_like(X)
+    if dC is not None:
+        _need(dC, "dC", X.dtype, C.shape, X.device)
+    elif want_dC:
+        dC = torch.empty_like(C)
+    lib, dt = _load(), _dt(X.dtype)
+    ws = _scratch(ws, lib.km_xent_grad_workspace_size(B, N, K, d, dt), X)
+    _check("km_xent_grad", lib.km_xent_grad(
+        X.data_ptr(), dt, C.data_ptr(), ids.data_ptr(), lse.data_ptr(), _a(g), B, N, K, d,
+        float(scale), _a(dX), _a(dC), ws.data_ptr(), ws.numel(), s))
     return dX, dC
 
 

@@ -949,9 +949,8 @@ km_status grad_sort(const int32_t *ids, int64_t B, int64_t N, int64_t K, const G
     s.K = static_cast<uint32_t>(K);
     s.width = p.width;
     if (p.small) {
-        if (cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kSmallSmem)) != cudaSuccess)
-            return KM_ERR_CUDA;
+        static std::atomic<uint64_t> ready{0};
+        if (!allow_smem(sort_small_kernel, kSmallSmem, ready)) return KM_ERR_CUDA;
         s.divE = make_fastdiv(static_cast<uint32_t>(ceil_div(T, kCluster * kSortThreads) * kSortThreads));
         // A zeroing block per 64 KB, but no more clusters than can be resident beside the sorting one:
         // a second wave would double the time.
@@ -987,10 +986,10 @@ km_status grad_sort(const int32_t *ids, int64_t B, int64_t N, int64_t K, const G
     }
     if ((zero && cudaMemsetAsync(zero, 0, zero_bytes, st) != cudaSuccess) ||
         cudaMemsetAsync(w.segtotal, 0, static_cast<size_t>(p.segs) * 4, st) != cudaSuccess ||
-        cudaMemsetAsync(w.jobs, 0, 4, st) != cudaSuccess ||
-        cudaFuncSetAttribute(sort_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSortSmem)) != cudaSuccess)
+        cudaMemsetAsync(w.jobs, 0, 4, st) != cudaSuccess)
         return KM_ERR_CUDA;
+    static std::atomic<uint64_t> ready{0};
+    if (!allow_smem(sort_scatter_kernel, kSortSmem, ready)) return KM_ERR_CUDA;
     s.n = static_cast<uint32_t>(p.n);
     s.segs = static_cast<uint32_t>(p.segs);
     s.tps = static_cast<uint32_t>(p.tps);

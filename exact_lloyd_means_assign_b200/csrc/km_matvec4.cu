@@ -500,15 +500,8 @@ km_status matvec4_simt(const void *xv, int64_t M, const uint8_t *packed, const f
 template <typename T, bool XV, int NT, int SC>
 km_status mma_launch(const CUtensorMap &tm, const T *x, MmaParams p, T *y, cudaStream_t st) {
     auto kernel = matvec4_mma_kernel<T, XV, NT, SC>;
-    static bool ready[64] = {false};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !ready[dev]) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMmaSmem)) !=
-            cudaSuccess)
-            return KM_ERR_CUDA;
-        if (dev >= 0 && dev < 64) ready[dev] = true;
-    }
+    static std::atomic<uint64_t> ready{0};
+    if (!allow_smem(kernel, kMmaSmem, ready)) return KM_ERR_CUDA;
     const int64_t rtiles = ceil_div(p.R, 16);
     if (rtiles > kMaxIndex / 4) return KM_ERR_UNSUPPORTED;
     // as many token tiles per launch as keep the item number below 2^30

@@ -27,17 +27,35 @@ inline int64_t piece_rows(int64_t B, int64_t N, int64_t K) {
     const int64_t fit = kPieceElems / (B * N) / kPieceStep * kPieceStep;
     return std::min(all, std::max<int64_t>(kPieceStep, fit));
 }
-// Splits of a product's reduction, each a multiple of 64 long: only where the output tiles alone
-// leave SMs idle, each split at least 512 long. The tensor cores work on 256 x 256 (or 128) tiles
-// per SM pair, the CUDA cores on 128 x 128 per SM.
+// Splits of a product's reduction, each a multiple of 64 long. The tensor cores work on 256 x 256 (or
+// 128) tiles, one SM pair each, of which 74 run at once: the split is the one with the shortest
+// estimate of waves * (64-wide steps of a split + 4 to start and drain) at 0.3 us a step, plus the
+// writing and reading of the splits' fp32 partials at 4 TB/s and a launch. (8192 x 4096 columns over
+// 32768 points at d = 128: two waves of 103 steps 72 us, one of 128 48 us.) The CUDA cores work on
+// 128 x 128 tiles and split where those leave SMs idle, each split at least 512 long.
 inline int64_t tc_bn_out(int64_t N) { return N > 128 ? 256 : 128; }
 inline int64_t product_splits(int64_t B, int64_t M, int64_t N, int64_t Kk, km_dtype dt) {
-    const int64_t tiles = dt == KM_F32 ? B * ceil_div(M, ST) * ceil_div(N, ST)
-                                       : 2 * B * ceil_div(M, 256) * ceil_div(N, tc_bn_out(N));
-    if (tiles >= 148) return 1;
-    const int64_t want = std::max<int64_t>(1, std::min(ceil_div(148, tiles), Kk / 512));
-    const int64_t per = ceil_div(ceil_div(Kk, TKC), want);
-    return ceil_div(ceil_div(Kk, TKC), per);
+    const int64_t steps = ceil_div(Kk, TKC);
+    if (dt == KM_F32) {
+        const int64_t tiles = B * ceil_div(M, ST) * ceil_div(N, ST);
+        if (tiles >= 148) return 1;
+        const int64_t want = std::max<int64_t>(1, std::min(ceil_div(148, tiles), Kk / 512));
+        return ceil_div(steps, ceil_div(steps, want));
+    }
+    const int64_t tiles = B * ceil_div(M, 256) * ceil_div(N, tc_bn_out(N));
+    int64_t best = 1;
+    double best_us = 0;
+    for (int64_t s = 1; s <= 64 && s <= steps; ++s) {
+        const int64_t per = ceil_div(steps, s), splits = ceil_div(steps, per);
+        if (splits != s) continue;      // the same pieces as with fewer splits
+        const double us = 0.3 * static_cast<double>(ceil_div(tiles * s, 74)) * static_cast<double>(per + 4) +
+                          (s > 1 ? 3.0 + 8e-6 / 4 * static_cast<double>(s * B * M * N) : 0.0);
+        if (s == 1 || us < best_us) {
+            best = s;
+            best_us = us;
+        }
+    }
+    return best;
 }
 
 // fp16 and bf16 run on the tensor cores. Rows that are no multiple of 16 bytes are copied to padded
@@ -140,9 +158,8 @@ km_status tc_launch(const Operand &A, const Operand &Bo, int64_t B, int64_t M, i
             return KM_ERR_CUDA;
     }
     auto kernel = tc_product_kernel<T, BN, MODE, AMN, BMN>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Sh::kTotal)) !=
-        cudaSuccess)
-        return KM_ERR_CUDA;
+    static std::atomic<uint64_t> ready{0};
+    if (!allow_smem(kernel, Sh::kTotal, ready)) return KM_ERR_CUDA;
     // persistent SM pairs: as many as can be resident (a pair needs two SMs of one GPC)
     static int resident[64] = {0};
     int dev = 0;
