@@ -5,6 +5,8 @@
 // T() rounds a codebook value to x's dtype, as the assignment rounds its centroids; the products
 // with the group scales and all sums are fp32. Two codes share a byte (even position in the low
 // half); rows are padded to 16 bytes so that every row starts on a vector boundary.
+#include <type_traits>
+
 #include "km_common.cuh"
 #include "km_host.h"
 
@@ -192,6 +194,14 @@ __device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity, volati
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     return mbar_wait_long(bar, parity, abort_flag);
 }
+
+}  // namespace mv4
+}  // namespace km
+
+#include "km_matvec4_tc.cuh"
+
+namespace km {
+namespace mv4 {
 
 // SC: 0 no scales, 1 groups of whole 128-code blocks, 2 any multiple of 32.
 template <typename T, bool XV, int NT, int SC>
@@ -479,6 +489,8 @@ namespace {
 
 using namespace km::mv4;
 
+constexpr int64_t kTcMinTokens = 8;
+
 inline int64_t pitch_of(int64_t N) { return ceil_div(N, 32) * 16; }
 
 template <typename T>
@@ -518,20 +530,120 @@ km_status mma_launch(const CUtensorMap &tm, const T *x, MmaParams p, T *y, cudaS
 }
 template <typename T, bool XV, int SC>
 km_status mma_tokens(const CUtensorMap &tm, const T *x, const MmaParams &p, T *y, cudaStream_t st) {
-    if (p.M <= 8) return mma_launch<T, XV, 1, SC>(tm, x, p, y, st);
-    if (p.M <= 16) return mma_launch<T, XV, 2, SC>(tm, x, p, y, st);
-    return mma_launch<T, XV, 4, SC>(tm, x, p, y, st);
+    if constexpr (!XV) {      // (with whole 16-byte rows, more tokens take the tcgen05 form)
+        if (p.M > 16) return mma_launch<T, XV, 4, SC>(tm, x, p, y, st);
+        if (p.M > kTcMinTokens) return mma_launch<T, XV, 2, SC>(tm, x, p, y, st);
+    }
+    return mma_launch<T, XV, 1, SC>(tm, x, p, y, st);
 }
 template <typename T, bool XV>
 km_status mma_scales(const CUtensorMap &tm, const T *x, const MmaParams &p, T *y, cudaStream_t st) {
     if (!p.scales) return mma_tokens<T, XV, 0>(tm, x, p, y, st);
     return p.cpg.d % 4 == 0 ? mma_tokens<T, XV, 1>(tm, x, p, y, st) : mma_tokens<T, XV, 2>(tm, x, p, y, st);
 }
+// tcgen05 form: rows of x in whole 16-byte units.
+template <typename T, int NTOK, int SC>
+km_status tc_launch(const uint8_t *packed, const T *x, TcMvParams p, T *y, cudaStream_t st) {
+    using L = TcMv<NTOK, SC>;
+    const EncodeTiledFn enc = encode_fn();
+    if (!enc) return KM_ERR_CUDA;
+    CUtensorMap tmW, tmX;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    {
+        const int64_t pitch = pitch_of(p.N);
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(p.R)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+        const cuuint32_t box[2] = {L::kStep / 2, kTcRows};
+        if (enc(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(packed), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, L::kStep == 256 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return KM_ERR_CUDA;
+    }
+    const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    {
+        // Rows of whole 64-position chunks: one copy brings a step's chunks of all tokens (chunks as a
+        // third index); else a copy per chunk, whose positions behind the row's end arrive as zeros.
+        p.x3d = p.N % 64 == 0 ? 1 : 0;
+        const cuuint64_t dims3[3] = {64, static_cast<cuuint64_t>(p.M), static_cast<cuuint64_t>(p.N / 64)};
+        const cuuint64_t strides3[2] = {static_cast<cuuint64_t>(p.N) * 2, 128};
+        const cuuint32_t box3[3] = {64, NTOK, L::kStep / 64};
+        const cuuint64_t dims2[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.M)};
+        if (enc(&tmX, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.x3d ? 3 : 2,
+                const_cast<T *>(x), p.x3d ? dims3 : dims2, strides3, box3, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return KM_ERR_CUDA;
+    }
+    p.svec = p.scales && p.ngroups % 4 == 0 && aligned(p.scales, 16) ? 1 : 0;
+    constexpr size_t smem = kTcEnd - 1024;      // the window's first 1024 bytes are the system's
+    auto kernel = matvec4_tc_kernel<T, NTOK, SC>;
+    static std::atomic<uint64_t> ready{0};
+    if (!allow_smem(kernel, smem, ready)) return KM_ERR_CUDA;
+    p.idesc = km::mma_idesc_f16(bf16 ? 1u : 0u, kTcRows, NTOK);
+    p.rtiles = static_cast<int>(ceil_div(p.R, kTcRows));
+    p.mtiles = static_cast<int>(ceil_div(p.M, NTOK));
+    p.steps = static_cast<int>(ceil_div(p.N, L::kStep));
+    const int64_t items = static_cast<int64_t>(p.rtiles) * p.mtiles;
+    if (items > kMaxIndex / 16) return KM_ERR_UNSUPPORTED;
+    // Few tiles: a cluster of 2, 4 or 8 blocks shares each, as long as all have an SM and two steps.
+    const int sms = num_sms();
+    p.split = 1;
+    while (p.split < 8 && items * p.split * 2 <= sms && p.steps >= p.split * 2 * 2) p.split *= 2;
+    p.sper = static_cast<int>(ceil_div(p.steps, p.split));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.split > 1 ? items * p.split : std::min<int64_t>(items, sms)));
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, static_cast<const TcMvParams &>(p), y) != cudaSuccess) {
+        cudaGetLastError();
+        return KM_ERR_CUDA;
+    }
+    return KM_OK;
+}
+template <typename T, int NTOK>
+km_status tc_scales(const uint8_t *packed, const T *x, const TcMvParams &p, T *y, cudaStream_t st) {
+    if (!p.scales) return tc_launch<T, NTOK, 0>(packed, x, p, y, st);
+    if (p.cpg.d % 4 == 0) return tc_launch<T, NTOK, 1>(packed, x, p, y, st);
+    return p.cpg.d % 2 == 0 ? tc_launch<T, NTOK, 2>(packed, x, p, y, st) : tc_launch<T, NTOK, 3>(packed, x, p, y, st);
+}
+template <typename T>
+km_status matvec4_tc(const T *x, int64_t M, const uint8_t *packed, const float *C, int64_t R, int64_t N, int64_t K,
+                     const float *scales, int64_t group, T *y, cudaStream_t st) {
+    TcMvParams p = {};
+    p.C = C;
+    p.scales = scales;
+    p.R = R;
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.ngroups = scales ? static_cast<int>(ceil_div(N, group)) : 0;
+    p.cpg = km::make_fastdiv(static_cast<uint32_t>(scales ? group / 32 : 4));
+    // as many tokens per launch as keep the item number small
+    const int64_t per = std::max<int64_t>(1, (int64_t{1} << 24) / ceil_div(R, kTcRows)) * 32;
+    for (int64_t m0 = 0; m0 < M; m0 += per) {
+        p.M = std::min(per, M - m0);
+        const km_status s = p.M <= 16 ? tc_scales<T, 16>(packed, x + m0 * N, p, y + m0 * R, st)
+                                      : tc_scales<T, 32>(packed, x + m0 * N, p, y + m0 * R, st);
+        if (s != KM_OK) return s;
+    }
+    return KM_OK;
+}
+
 template <typename T>
 km_status matvec4_mma(const void *xv, int64_t M, const uint8_t *packed, const float *C, int64_t R, int64_t N,
                       int64_t K, const float *scales, int64_t group, void *yv, cudaStream_t st) {
     const T *x = static_cast<const T *>(xv);
     T *y = static_cast<T *>(yv);
+    const bool xvec = N % 8 == 0 && aligned(x, 16);
+    // more than one token tile of the mma.sync form: the tcgen05 form decodes once for all of them
+    if (xvec && M > kTcMinTokens) return matvec4_tc<T>(x, M, packed, C, R, N, K, scales, group, y, st);
     const EncodeTiledFn enc = encode_fn();
     if (!enc) return KM_ERR_CUDA;
     CUtensorMap tm;
@@ -552,7 +664,7 @@ km_status matvec4_mma(const void *xv, int64_t M, const uint8_t *packed, const fl
     p.K = static_cast<int>(K);
     p.ngroups = scales ? static_cast<int>(ceil_div(N, group)) : 0;
     p.cpg = km::make_fastdiv(static_cast<uint32_t>(scales ? group / 32 : 4));
-    return N % 8 == 0 && aligned(x, 16) ? mma_scales<T, true>(tm, x, p, y, st) : mma_scales<T, false>(tm, x, p, y, st);
+    return xvec ? mma_scales<T, true>(tm, x, p, y, st) : mma_scales<T, false>(tm, x, p, y, st);
 }
 
 }  // namespace
