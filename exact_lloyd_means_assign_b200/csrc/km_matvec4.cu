@@ -33,61 +33,77 @@ __global__ void __launch_bounds__(256)
     packed[u] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// CUDA-core form: one warp per row, eight consecutive codes per lane and step. The row's 16
-// codebook values lie in 16 different banks, so the 32 lanes' lookups never conflict.
-constexpr int kSimtWarps = 4;
+// fp32 tokens, on the CUDA cores: a warp per row, eight consecutive codes per lane and step. The
+// row's 16 codebook values lie in 16 different banks, so the 32 lanes' lookups never conflict.
+// The tokens are staged in shared memory kSimtChunk positions at a time, every group of eight in two
+// 16-byte halves 16 * kSimtChunk / 8 bytes apart, which a warp reads without conflicts; the codes of
+// the next chunk are read before that. (1003 rows x 1999, three tokens: with the tokens read from
+// L2 element by element 17.5 us, staged 9.8.)
+constexpr int kSimtWarps = 8;
+constexpr int kSimtChunk = 1024;
 
-template <typename T, int MT>
+template <int MT>
 __global__ void __launch_bounds__(32 * kSimtWarps)
-    matvec4_simt_kernel(const T *__restrict__ x, int64_t M, const uint8_t *__restrict__ packed, int64_t pitch,
-                        const float *__restrict__ C, int64_t R, int N, int K, const float *__restrict__ scales,
-                        int group, int ngroups, bool xvec, T *__restrict__ y) {
+    matvec4_f32_kernel(const float *__restrict__ x, int64_t M, const uint8_t *__restrict__ packed, int64_t pitch,
+                       const float *__restrict__ C, int64_t R, int N, int K, const float *__restrict__ scales,
+                       FastDiv cpg, int ngroups, float *__restrict__ y) {
+    constexpr int kSteps = kSimtChunk / 256;
     __shared__ float tab[kSimtWarps][kKmax];
+    __shared__ float4 xs[MT][2][kSimtChunk / 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * kSimtWarps + warp;
-    if (r >= R) return;
-    if (lane < kKmax) tab[warp][lane] = lane < K ? round_through<T>(C[r * K + lane]) : 0.f;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * kSimtWarps + warp, rr = min(r, R - 1);
+    if (lane < kKmax) tab[warp][lane] = lane < K ? C[rr * K + lane] : 0.f;
     __syncwarp();
-    const uint32_t *row = reinterpret_cast<const uint32_t *>(packed + r * pitch);
-    const float *srow = scales ? scales + r * ngroups : nullptr;
-    for (int64_t m0 = 0; m0 < M; m0 += MT) {
-        float acc[MT];
+    const uint32_t *row = reinterpret_cast<const uint32_t *>(packed + rr * pitch);
+    const float *srow = scales ? scales + rr * ngroups : nullptr;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * MT;
+    uint32_t next[kSteps];
+    auto read_codes = [&](int n0) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m] = 0.f;
-#pragma unroll 2
-        for (int n = lane * 8; n < N; n += 256) {
-            const uint32_t w = row[n >> 3];
-            float part[MT];
+        for (int i = 0; i < kSteps; ++i) {
+            const int n = n0 + i * 256 + lane * 8;
+            next[i] = n < N ? __ldg(row + (n >> 3)) : 0u;
+        }
+    };
+    read_codes(0);
+    float acc[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) part[m] = 0.f;
-            const bool whole = xvec && n + 8 <= N;
+    for (int m = 0; m < MT; ++m) acc[m] = 0.f;
+    for (int n0 = 0; n0 < N; n0 += kSimtChunk) {
+        uint32_t w[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) w[i] = next[i];
+        __syncthreads();      // the chunk before is used up
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            for (int i = threadIdx.x; i < kSimtChunk; i += 32 * kSimtWarps) {
+                const float v = n0 + i < N && m0 + m < M ? __ldg(x + (m0 + m) * N + n0 + i) : 0.f;
+                reinterpret_cast<float *>(&xs[m][(i >> 2) & 1][i >> 3])[i & 3] = v;
+            }
+        if (n0 + kSimtChunk < N) read_codes(n0 + kSimtChunk);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int n = n0 + i * 256 + lane * 8;
+            if (n >= N) break;
+            float c[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                c[j] = n + j < N ? tab[warp][(w[i] >> (4 * j)) & 15] : 0.f;   // (none behind the row's end)
+            const float s = srow ? __ldg(srow + fd_div(cpg, n >> 5)) : 1.f;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                if (m0 + m >= M) continue;
-                const T *xr = x + (m0 + m) * N + n;
-                if (whole) {
-                    struct alignas(sizeof(T) * 4) V4 { T v[4]; };
-                    const V4 a = *reinterpret_cast<const V4 *>(xr), b = *reinterpret_cast<const V4 *>(xr + 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        part[m] = fmaf(tab[warp][(w >> (4 * j)) & 15], Cvt<T>::to_f(a.v[j]), part[m]);
-                        part[m] = fmaf(tab[warp][(w >> (4 * j + 16)) & 15], Cvt<T>::to_f(b.v[j]), part[m]);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (n + j < N) part[m] = fmaf(tab[warp][(w >> (4 * j)) & 15], Cvt<T>::to_f(xr[j]), part[m]);
-                }
+                const float4 a = xs[m][0][i * 32 + lane], b = xs[m][1][i * 32 + lane];
+                const float p = fmaf(c[3], a.w, fmaf(c[2], a.z, fmaf(c[1], a.y, c[0] * a.x))) +
+                                fmaf(c[7], b.w, fmaf(c[6], b.z, fmaf(c[5], b.y, c[4] * b.x)));
+                acc[m] = fmaf(s, p, acc[m]);
             }
-            const float s = srow ? srow[n / group] : 1.f;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m] = fmaf(s, part[m], acc[m]);
         }
+    }
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const float t = warp_sum(acc[m]);
-            if (lane == 0 && m0 + m < M) y[(m0 + m) * R + r] = Cvt<T>::from_f(t);
-        }
+    for (int m = 0; m < MT; ++m) {
+        const float t = warp_sum(acc[m]);
+        if (lane == 0 && r < R && m0 + m < M) y[(m0 + m) * R + r] = t;
     }
 }
 
@@ -489,24 +505,34 @@ namespace {
 
 using namespace km::mv4;
 
-constexpr int64_t kTcMinTokens = 8;
+// The tcgen05 form decodes once for all tokens, where the mma.sync form pays for every eight, but it
+// takes some 8 us to start and end. GPU times, tcgen05 / mma.sync: 16 tokens x 8192 x 8192 21 / 32 us,
+// x 4096 x 4096 13.5 / 8.8; 32 tokens x 8192 x 8192 26 / 46, x 4096 x 4096 23 / 19.
+constexpr int64_t kTcMinTokens = 8, kTcMinWeights = int64_t{1} << 25;
 
 inline int64_t pitch_of(int64_t N) { return ceil_div(N, 32) * 16; }
 
-template <typename T>
-km_status matvec4_simt(const void *xv, int64_t M, const uint8_t *packed, const float *C, int64_t R, int64_t N,
-                       int64_t K, const float *scales, int64_t group, void *yv, cudaStream_t st) {
-    const T *x = static_cast<const T *>(xv);
-    T *y = static_cast<T *>(yv);
-    const int ng = scales ? static_cast<int>(ceil_div(N, group)) : 0;
-    const bool xvec = N % 4 == 0 && aligned(x, 4 * sizeof(T));
-    const unsigned grid = static_cast<unsigned>(ceil_div(R, kSimtWarps));
-    const int g = static_cast<int>(group), Ni = static_cast<int>(N), Ki = static_cast<int>(K);
-    if (M == 1)
-        matvec4_simt_kernel<T, 1><<<grid, 32 * kSimtWarps, 0, st>>>(x, M, packed, pitch_of(N), C, R, Ni, Ki, scales, g, ng, xvec, y);
-    else
-        matvec4_simt_kernel<T, 4><<<grid, 32 * kSimtWarps, 0, st>>>(x, M, packed, pitch_of(N), C, R, Ni, Ki, scales, g, ng, xvec, y);
-    return launch_status();
+template <int MT>
+km_status f32_launch(const float *x, int64_t M, const uint8_t *packed, const float *C, int64_t R, int64_t N, int64_t K,
+                     const float *scales, int64_t group, float *y, cudaStream_t st) {
+    const int64_t blocks = ceil_div(R, kSimtWarps), per = static_cast<int64_t>(kMaxGridY) * MT;
+    for (int64_t m0 = 0; m0 < M; m0 += per) {
+        const int64_t mn = std::min(per, M - m0);
+        const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(ceil_div(mn, MT)));
+        matvec4_f32_kernel<MT><<<grid, 32 * kSimtWarps, 0, st>>>(
+            x + m0 * N, mn, packed, pitch_of(N), C, R, static_cast<int>(N), static_cast<int>(K), scales,
+            km::make_fastdiv(static_cast<uint32_t>(scales ? group / 32 : 1)),
+            scales ? static_cast<int>(ceil_div(N, group)) : 0, y + m0 * R);
+        if (launch_status() != KM_OK) return KM_ERR_CUDA;
+    }
+    return KM_OK;
+}
+km_status matvec4_f32(const void *xv, int64_t M, const uint8_t *packed, const float *C, int64_t R, int64_t N, int64_t K,
+                      const float *scales, int64_t group, void *yv, cudaStream_t st) {
+    const float *x = static_cast<const float *>(xv);
+    float *y = static_cast<float *>(yv);
+    if (M == 1) return f32_launch<1>(x, M, packed, C, R, N, K, scales, group, y, st);
+    return f32_launch<4>(x, M, packed, C, R, N, K, scales, group, y, st);
 }
 
 template <typename T, bool XV, int NT, int SC>
@@ -530,11 +556,9 @@ km_status mma_launch(const CUtensorMap &tm, const T *x, MmaParams p, T *y, cudaS
 }
 template <typename T, bool XV, int SC>
 km_status mma_tokens(const CUtensorMap &tm, const T *x, const MmaParams &p, T *y, cudaStream_t st) {
-    if constexpr (!XV) {      // (with whole 16-byte rows, more tokens take the tcgen05 form)
-        if (p.M > 16) return mma_launch<T, XV, 4, SC>(tm, x, p, y, st);
-        if (p.M > kTcMinTokens) return mma_launch<T, XV, 2, SC>(tm, x, p, y, st);
-    }
-    return mma_launch<T, XV, 1, SC>(tm, x, p, y, st);
+    if (p.M <= 8) return mma_launch<T, XV, 1, SC>(tm, x, p, y, st);
+    if (p.M <= 16) return mma_launch<T, XV, 2, SC>(tm, x, p, y, st);
+    return mma_launch<T, XV, 4, SC>(tm, x, p, y, st);
 }
 template <typename T, bool XV>
 km_status mma_scales(const CUtensorMap &tm, const T *x, const MmaParams &p, T *y, cudaStream_t st) {
@@ -642,8 +666,7 @@ km_status matvec4_mma(const void *xv, int64_t M, const uint8_t *packed, const fl
     const T *x = static_cast<const T *>(xv);
     T *y = static_cast<T *>(yv);
     const bool xvec = N % 8 == 0 && aligned(x, 16);
-    // more than one token tile of the mma.sync form: the tcgen05 form decodes once for all of them
-    if (xvec && M > kTcMinTokens) return matvec4_tc<T>(x, M, packed, C, R, N, K, scales, group, y, st);
+    if (xvec && M > kTcMinTokens && R * N >= kTcMinWeights) return matvec4_tc<T>(x, M, packed, C, R, N, K, scales, group, y, st);
     const EncodeTiledFn enc = encode_fn();
     if (!enc) return KM_ERR_CUDA;
     CUtensorMap tm;
@@ -704,7 +727,7 @@ km_status km_matvec4(const void *x, km_dtype dtype, int64_t M, const uint8_t *pa
         return KM_ERR_INVALID_ARG;
     if (K > kKmax || (scales && group % 32 != 0)) return KM_ERR_UNSUPPORTED;
     switch (dtype) {
-        case KM_F32: return matvec4_simt<float>(x, M, packed, C, R, N, K, scales, group, y, S(stream));
+        case KM_F32: return matvec4_f32(x, M, packed, C, R, N, K, scales, group, y, S(stream));
         case KM_F16: return matvec4_mma<__half>(x, M, packed, C, R, N, K, scales, group, y, S(stream));
         default: return matvec4_mma<__nv_bfloat16>(x, M, packed, C, R, N, K, scales, group, y, S(stream));
     }

@@ -56,6 +56,48 @@ def test_matvec4(cuda_device, dtype, R, N, M, K, group):
     assert torch.equal(y, km.km_matvec4(x, packed, C, s, group))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("R,N,M,K,group", [
+    (8192, 4096, 9, 16, 128), (8200, 4104, 16, 16, 64), (4100, 8200, 12, 15, 32), (16500, 2048, 33, 16, 0),
+    (2049, 16392, 17, 16, 96), (1024, 32768, 40, 16, 256), (300000, 120, 10, 16, 32), (129, 262144, 9, 4, 4096),
+    (33000, 1032, 32, 16, 160)])
+def test_more_tokens_on_large_weights(cuda_device, dtype, R, N, M, K, group):
+    # the form that decodes into tensor memory: few and many row tiles, reductions shared by a
+    # cluster, every class of scale groups, ragged rows, steps and tokens; rows sampled
+    codes, C, x, s = _inputs(R, N, M, K, group, dtype, cuda_device, seed=R + N + M)
+    packed = km.km_pack4(codes)
+    y = km.km_matvec4(x, packed, C, s, group)
+    torch.cuda.synchronize()
+    assert km.km_device_error() == 0
+    g = torch.Generator().manual_seed(1)
+    rows = torch.unique(torch.cat([torch.arange(0, min(R, 3)), torch.arange(max(0, R - 130), R),
+                                   torch.randint(0, R, (200,), generator=g)])).to(cuda_device)
+    _check(y[:, rows], x, codes[rows], C[rows], None if s is None else s[rows], group)
+    assert torch.equal(y, km.km_matvec4(x, packed, C, s, group))
+    # every token's result is that of the token alone, up to the order of the sums
+    one = km.km_matvec4(x[-1:].contiguous(), packed, C, s, group)
+    _check(one[:, rows], x[-1:], codes[rows], C[rows], None if s is None else s[rows], group)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_infinities_stay_in_their_row_of_large_weights(cuda_device, dtype):
+    R, N, M, group = 8192, 4168, 11, 128
+    codes, C, x, s = _inputs(R, N, M, 15, group, dtype, cuda_device, seed=16)
+    full = torch.cat([C, torch.full((R, 1), float("inf"), device=cuda_device)], 1).contiguous()   # code 15, unused
+    full[7, 0] = float("inf")               # code 0 is also what the padding holds
+    codes[7] = torch.where(codes[7] == 0, torch.ones_like(codes[7]), codes[7])
+    s[130] = float("nan")
+    x[4] = float("nan")
+    x[6, 17] = float("inf")
+    y = km.km_matvec4(x, km.km_pack4(codes), full, s, group).float()
+    torch.cuda.synchronize()
+    toks, rows = torch.ones(M, dtype=torch.bool), torch.ones(R, dtype=torch.bool)
+    toks[4] = toks[6] = False
+    rows[130] = False
+    assert torch.isnan(y[4]).all() and torch.isnan(y[:, 130]).all() and not torch.isfinite(y[6]).any()
+    assert torch.isfinite(y.cpu()[toks][:, rows]).all()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_codes_beyond_the_codebook_stand_for_zero(cuda_device, dtype):
     codes, C, x, _ = _inputs(20, 300, 2, 16, 0, dtype, cuda_device, seed=5)
