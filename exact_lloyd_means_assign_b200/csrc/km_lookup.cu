@@ -670,6 +670,10 @@ __global__ void __launch_bounds__(kGradThreads)
     } else {
         s = range_begin<LPR>(p.keys, n, first, p.range, cut0);
         len = range_begin<LPR>(p.keys, n, first + p.range, p.range, cut1) - s;   // at most two ranges' entries
+        if (t < len) {
+            key0 = p.keys[s + t];
+            pos0 = p.pos[s + t];
+        }
     }
     const uint32_t c = blockIdx.y * LPR + t;
     const bool in = c < p.units;
@@ -690,11 +694,11 @@ __global__ void __launch_bounds__(kGradThreads)
         }
     };
     for (uint32_t b = 0; __any_sync(0xffffffffu, b < len); b += LPR) {
-        const bool have = b + t < len;
-        uint32_t key = key0, pos = pos0;
-        if (!SHORT) {
-            key = have ? p.keys[s + b + t] : 0;
-            pos = have ? p.pos[s + b + t] : 0;
+        // this batch's entries were read while the one before was summed
+        const uint32_t key = key0, pos = pos0;
+        if (!SHORT && b + LPR + t < len) {
+            key0 = p.keys[s + b + LPR + t];
+            pos0 = p.pos[s + b + LPR + t];
         }
         if (b == 0) cur = __shfl_sync(0xffffffffu, key, 0, LPR);
 #pragma unroll 1

@@ -295,7 +295,8 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
     const bool tc = use_tc(dt, d, scale, X, C);
     const int64_t dp = tc ? padded(d, dt) : d;
     km_status s;
-    unsigned int *wmax = dt == KM_F16 ? w.wmax : nullptr;
+    unsigned int *wmax = dt != KM_F32 ? w.wmax : nullptr;
+    const float pscale = dt == KM_F16 ? 16384.f : 1.f;
     if (wmax && cudaMemsetAsync(wmax, 0, 4, st) != cudaSuccess) return KM_ERR_CUDA;
     km::xe::weight_kernel<<<static_cast<unsigned>(ceil_div(B * N, 256)), 256, 0, st>>>(
         g, ids, B * N, static_cast<int>(K), scale, w.w, wmax);
@@ -323,11 +324,13 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
         p.P = w.P;
         p.ldp = kc;
         p.wmax = wmax;
+        p.pscale = pscale;
         s = product<T, kProb>(tc, Operand{X, N * dp, dp, 1}, Operand{Ck, K * dp, dp, 1}, B, N, kn, dp, p, 1, st);
         if (s != KM_OK) return s;
         if (dX) {
             Epi q = {};
             q.wmax = wmax;
+            q.pscale = pscale;
             q.acc = k0 ? w.dxacc : nullptr;
             if (k0 + kc < K) q.out32 = w.dxacc;
             else q.outT = dX;
@@ -340,6 +343,7 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
             // piece is the whole table
             Epi q = {};
             q.wmax = wmax;
+            q.pscale = pscale;
             const int64_t nb = kn == K ? B : 1;
             for (int64_t b = 0; b < B; b += nb) {
                 q.outT = static_cast<T *>(dC) + (b * K + k0) * d;

@@ -34,22 +34,24 @@ struct Epi {
     void *P;               // [B, M, ldp]
     int64_t ldp;
     // kOut: out = acc (fp32) + value / f, or the fp32 partial of one split of the reduction
-    const unsigned int *wmax;   // bits of max |w| (16-bit floats with a 5-bit exponent), or null
+    const unsigned int *wmax;   // bits of max |w| (16-bit points), or null
+    float pscale;          // s of p_factor
     const float *acc;      // added, or null
     float *out32;          // fp32 result or partials [split][B][M][N], or null
     void *outT;            // result in the points' type, or null
     int splits;
 };
 
-// P is held in the points' type. With fp16 its entries, probabilities times gradients, would fall
-// below the type's normal range, so they are scaled by a power of two that takes max |w| to
-// [2^14, 2^15) (|P| <= |w|, so nothing overflows) and the products are scaled back; both
-// scalings are exact.
-__device__ __forceinline__ float pow2_factor(const unsigned int *wmax, bool inverse) {
+// With 16-bit points P is held relative to the largest weight: P = (w_n / max |w|) s (p - [label]).
+// The label's entry is the largest of its row, about -w_n, and in a mean of losses all w_n are
+// equal: rounded as they are, every token's largest term would be off by the same fraction of
+// itself (half a step of the type), which no sum over tokens averages away; relative to the maximum it
+// is near -1, which has none of that. s is 1, and 2^14 for fp16, whose normal range ends at 2^-14:
+// probabilities down to 2^-28 keep their bits. The products are multiplied by max |w| / s in fp32.
+__device__ __forceinline__ float p_factor(const unsigned int *wmax, float s, bool inverse) {
     if (!wmax) return 1.f;
-    int e = 14 - (static_cast<int>(*wmax >> 23) - 127);
-    e = max(-100, min(100, e));
-    return __int_as_float((127 + (inverse ? -e : e)) << 23);
+    const float m = fminf(fmaxf(__uint_as_float(*wmax), 0x1p-100f), 0x1p100f);
+    return inverse ? m / s : s / m;
 }
 
 // ------------------------------------------------------------------ CUDA-core products
@@ -121,8 +123,8 @@ __global__ void __launch_bounds__(kSimtThreads)
         }
         __syncthreads();
     }
-    const float inv = MODE == kOut && p.splits == 1 ? pow2_factor(p.wmax, true) : 1.f;
-    const float fac = MODE == kProb ? pow2_factor(p.wmax, false) : 1.f;
+    const float inv = MODE == kOut && p.splits == 1 ? p_factor(p.wmax, p.pscale, true) : 1.f;
+    const float fac = MODE == kProb ? p_factor(p.wmax, p.pscale, false) : 1.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = m0 + (i & 3) + ty * 4 + (i >> 2) * 64;
@@ -240,7 +242,8 @@ __global__ void __launch_bounds__(256)
         w[i] = v;
     }
     if (wmax) {
-        const unsigned int m = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v)));
+        // (a weight that is not finite spoils its own terms only)
+        const unsigned int m = __reduce_max_sync(0xffffffffu, isfinite(v) ? __float_as_uint(fabsf(v)) : 0u);
         if ((threadIdx.x & 31) == 0 && m) atomicMax(wmax, m);
     }
 }
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(256)
 template <typename T>
 __global__ void __launch_bounds__(256)
     split_join_kernel(const float *__restrict__ parts, int splits, int64_t count, Epi p) {
-    const float inv = pow2_factor(p.wmax, true);
+    const float inv = p_factor(p.wmax, p.pscale, true);
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
         float v = 0.f;
         for (int s = 0; s < splits; ++s) v += parts[s * count + i];

@@ -267,8 +267,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
         // The products are formed with |scale| (a negative scale negates the points in the MMA).
         const float sc = fabsf(ep.scale), s2 = sc * kLog2e;
         const uint64_t s22 = pair_f32(s2, s2);
-        const float fac = MODE == kProb ? pow2_factor(ep.wmax, false) : 1.f;
-        const float inv = MODE == kOut && ep.splits == 1 ? pow2_factor(ep.wmax, true) : 1.f;
+        const float fac = MODE == kProb ? p_factor(ep.wmax, ep.pscale, false) : 1.f;
+        const float inv = MODE == kOut && ep.splits == 1 ? p_factor(ep.wmax, ep.pscale, true) : 1.f;
         const uint32_t obuf = sbase + Sh::kOutOff + (warp - T_EPI0) * 2 * kOutBuf;
         int buf = 0, ob = 0;
         uint32_t aph = 0;

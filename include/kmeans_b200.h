@@ -441,9 +441,8 @@ km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int
  *     dX[b,n] = sum_k P[n,k] C[b,k],      dC[b,k] = sum_n P[n,k] X[b,n].
  * lse as km_xent wrote it; g[B,N] fp32, the gradient of each loss, NULL = all ones; dX[B,N,d],
  * dC[B,K,d] in `dtype`, either may be NULL. The logits are computed again, one piece of the table
- * at a time, and P is held in `dtype` (fp16: scaled by a power of two that takes the largest
- * |g * scale| to [2^14, 2^15), so that small probabilities keep their bits); all sums are fp32,
- * in an order fixed by the sizes. Points without a label may hold any values: they reach
+ * at a time, and P is held in `dtype`, relative to the largest |g * scale| (fp16: times 2^14, so
+ * that small probabilities keep their bits); all sums are fp32, in an order fixed by the sizes. Points without a label may hold any values: they reach
  * neither gradient (their own rows of dX are zero).
  *
  * ws: km_xent_workspace_size / km_xent_grad_workspace_size bytes, 256-byte aligned (0 for sizes
