@@ -1,10 +1,12 @@
 // km_xent.cu -- softmax cross entropy over a table: C entry points, workspaces and launches
 // (kernels in km_xent.cuh).
+#include <cmath>
 #include <type_traits>
 
 #include "km_host.h"
 #include "km_xent.cuh"
 #include "km_xent_tc.cuh"
+#include "km_xent_fused.cuh"
 
 namespace {
 
@@ -27,13 +29,13 @@ inline int64_t piece_rows(int64_t B, int64_t N, int64_t K) {
     const int64_t fit = kPieceElems / (B * N) / kPieceStep * kPieceStep;
     return std::min(all, std::max<int64_t>(kPieceStep, fit));
 }
-// Splits of a product's reduction, each a multiple of 64 long. The tensor cores work on 256 x 256 (or
-// 128) tiles, one SM pair each, of which 74 run at once: the split is the one with the shortest
-// estimate of waves * (64-wide steps of a split + 4 to start and drain) at 0.3 us a step, plus the
-// writing and reading of the splits' fp32 partials at 4 TB/s and a launch. (8192 x 4096 columns over
-// 32768 points at d = 128: two waves of 103 steps 72 us, one of 128 48 us.) The CUDA cores work on
-// 128 x 128 tiles and split where those leave SMs idle, each split at least 512 long.
-inline int64_t tc_bn_out(int64_t N) { return N > 128 ? 256 : 128; }
+// Splits of a product's reduction, each a multiple of 64 long. The tensor cores work on 256 x 256
+// tiles, one SM pair each, of which 74 run at once: the split is the one with the shortest estimate of
+// waves * (64-wide steps of a split + 4 to start and drain) at 0.3 us a step, plus the writing and
+// reading of the splits' fp32 partials at 4 TB/s and a launch. (dC of a 4096-row table over 32768 points
+// at d = 256, 16 tiles: 253 us unsplit, 161 in the chosen four; dX, 128 tiles: 152 unsplit as chosen, 189 in
+// two.) The CUDA cores work on 128 x 128 tiles and split where those leave SMs idle, each split at least
+// 512 long.
 inline int64_t product_splits(int64_t B, int64_t M, int64_t N, int64_t Kk, km_dtype dt) {
     const int64_t steps = ceil_div(Kk, TKC);
     if (dt == KM_F32) {
@@ -42,7 +44,7 @@ inline int64_t product_splits(int64_t B, int64_t M, int64_t N, int64_t Kk, km_dt
         const int64_t want = std::max<int64_t>(1, std::min(ceil_div(148, tiles), Kk / 512));
         return ceil_div(steps, ceil_div(steps, want));
     }
-    const int64_t tiles = B * ceil_div(M, 256) * ceil_div(N, tc_bn_out(N));
+    const int64_t tiles = B * ceil_div(M, 2 * TBM) * ceil_div(N, TBN);
     int64_t best = 1;
     double best_us = 0;
     for (int64_t s = 1; s <= 64 && s <= steps; ++s) {
@@ -79,6 +81,38 @@ inline LossWs carve_loss(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d, 
     w.pairs = c.take<float2>(static_cast<size_t>(B * ceil_div(K, ST) * N) * 8);
     w.zt = c.take<float>(static_cast<size_t>(B * N) * 4);
     return w;
+}
+
+// Gradients of rows of up to 128 16-bit values take the fused form (three tiles of S and one of O fill
+// TMEM; longer rows leave the exponentials the smaller part). 32768 points x 8192 rows at d = 128: dX
+// 146 us against 270 through P in memory, dC 149 against 268; 20000 x 300: dX 31 against 27, dC 31 against
+// 36; 100000 x 64 at d = 32: dX 38 against 39, dC 48 against 50.
+inline bool fused_shape(km_dtype dt, int64_t d) { return dt != KM_F32 && d <= 128; }
+// Blocks of one gradient: all SMs, but two tiles at least for each.
+// (The tiles of both directions number the same, below 2^31 by xent_sizes_ok.)
+inline int fused_tiles(int64_t B, int64_t M, int64_t cols) {
+    static_assert(FR == ST, "xent_sizes_ok counts tiles of ST");
+    return static_cast<int>(B * ceil_div(M, FR) * ceil_div(cols, FR));
+}
+inline int fused_blocks(int tiles) { return std::min(num_sms(), tiles / 2 + tiles % 2); }
+struct FusedWs {
+    void *X, *C;
+    float *w, *parts;
+    unsigned int *wmax;
+    PointTile *points;
+    int64_t ptiles;
+};
+inline FusedWs carve_fused(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d, km_dtype dt) {
+    FusedWs f;
+    const int64_t dp = padded(d, dt);
+    f.ptiles = ceil_div(N, FR);
+    f.X = c.take<uint8_t>(static_cast<size_t>(B * N * dp) * 2);
+    f.C = c.take<uint8_t>(static_cast<size_t>(B * K * dp) * 2);
+    f.w = c.take<float>(static_cast<size_t>(B * N) * 4);
+    f.wmax = c.take<unsigned int>(4);
+    f.points = c.take<PointTile>(static_cast<size_t>(B * f.ptiles) * sizeof(PointTile));
+    f.parts = c.take<float>(static_cast<size_t>(fused_blocks(fused_tiles(B, N, K))) * 2 * FR * (d > 64 ? 128 : 64) * 4);
+    return f;
 }
 
 struct GradWs {
@@ -138,14 +172,14 @@ inline bool encode_operand(CUtensorMap *tm, CUtensorMapDataType tdt, const Opera
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int BN, int MODE, bool AMN, bool BMN>
+template <typename T, int MODE, bool AMN, bool BMN>
 km_status tc_launch(const Operand &A, const Operand &Bo, int64_t B, int64_t M, int64_t N, int64_t Kk, Epi e,
                     int64_t splits, cudaStream_t st) {
-    using Sh = TcShape<BN, MODE>;
+    using Sh = TcShape<MODE>;
     const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     const CUtensorMapDataType tdt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap tmA, tmB;
-    if (!encode_operand(&tmA, tdt, A, M, Kk, B, TBM) || !encode_operand(&tmB, tdt, Bo, N, Kk, B, BN / 2))
+    if (!encode_operand(&tmA, tdt, A, M, Kk, B, TBM) || !encode_operand(&tmB, tdt, Bo, N, Kk, B, TBN / 2))
         return KM_ERR_CUDA;
     CUtensorMap tmP = tmA;      // (read where P is written only)
     if (MODE == kProb) {
@@ -157,7 +191,7 @@ km_status tc_launch(const Operand &A, const Operand &Bo, int64_t B, int64_t M, i
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return KM_ERR_CUDA;
     }
-    auto kernel = tc_product_kernel<T, BN, MODE, AMN, BMN>;
+    auto kernel = tc_product_kernel<T, MODE, AMN, BMN>;
     static std::atomic<uint64_t> ready{0};
     if (!allow_smem(kernel, Sh::kTotal, ready)) return KM_ERR_CUDA;
     // persistent SM pairs: as many as can be resident (a pair needs two SMs of one GPC)
@@ -187,12 +221,12 @@ km_status tc_launch(const Operand &A, const Operand &Bo, int64_t B, int64_t M, i
     p.M = static_cast<int>(M);
     p.N = static_cast<int>(N);
     p.mt = static_cast<int>(ceil_div(M, 2 * TBM));
-    p.nt = static_cast<int>(ceil_div(N, BN));
+    p.nt = static_cast<int>(ceil_div(N, TBN));
     p.nb = static_cast<int>(B);
     p.Kk = static_cast<int>(Kk);
     p.kchunks = static_cast<int>(ceil_div(Kk, TKC));
     p.kper = static_cast<int>(ceil_div(p.kchunks, splits));
-    p.idesc = km::mma_idesc_f16(bf16 ? 1u : 0u, 2 * TBM, BN) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
+    p.idesc = km::mma_idesc_f16(bf16 ? 1u : 0u, 2 * TBM, TBN) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
               (MODE != kOut && e.scale < 0.f ? 1u << 13 : 0u);   // bit 13 negates A
     p.vec = N % 8 == 0 && (!e.outT || aligned(e.outT, 16)) ? 1 : 0;
     e.splits = static_cast<int>(splits);
@@ -213,14 +247,10 @@ km_status product(bool tc, const Operand &A, const Operand &Bo, int64_t B, int64
     if constexpr (!std::is_same<T, float>::value) {
         if (tc) {
             if constexpr (MODE != kOut) {
-                return tc_launch<T, 256, MODE, false, false>(A, Bo, B, M, N, Kk, p, splits, st);
+                return tc_launch<T, MODE, false, false>(A, Bo, B, M, N, Kk, p, splits, st);
             } else {
-                const bool wide = tc_bn_out(N) == 256;
-                if (A.k_s == 1)     // dX = P C
-                    return wide ? tc_launch<T, 256, kOut, false, true>(A, Bo, B, M, N, Kk, p, splits, st)
-                                : tc_launch<T, 128, kOut, false, true>(A, Bo, B, M, N, Kk, p, splits, st);
-                return wide ? tc_launch<T, 256, kOut, true, true>(A, Bo, B, M, N, Kk, p, splits, st)
-                            : tc_launch<T, 128, kOut, true, true>(A, Bo, B, M, N, Kk, p, splits, st);
+                if (A.k_s == 1) return tc_launch<T, kOut, false, true>(A, Bo, B, M, N, Kk, p, splits, st);   // dX = P C
+                return tc_launch<T, kOut, true, true>(A, Bo, B, M, N, Kk, p, splits, st);
             }
         }
     }
@@ -286,10 +316,96 @@ km_status loss_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
     return launch_status();
 }
 
+// One gradient of the fused form: rows of A against all rows of B.
+template <typename T, int DN, bool COL>
+km_status fused_launch(const void *A, const void *Bo, int64_t B, int64_t M, int64_t cols, int64_t d, int64_t dp, float scale,
+                       const FusedWs &w, float pscale, void *out, cudaStream_t st) {
+    using Sh = FShape<DN, COL>;
+    const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    const CUtensorMapDataType tdt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap tmA, tmB;
+    if (!encode_operand(&tmA, tdt, Operand{A, M * dp, dp, 1}, M, dp, B, FR) ||
+        !encode_operand(&tmB, tdt, Operand{Bo, cols * dp, dp, 1}, cols, dp, B, FR))
+        return KM_ERR_CUDA;
+    auto kernel = fused_grad_kernel<T, DN, COL>;
+    static std::atomic<uint64_t> ready{0};
+    if (!allow_smem(kernel, Sh::kTotal, ready)) return KM_ERR_CUDA;
+    FParams p = {};
+    p.M = static_cast<int>(M);
+    p.cols = static_cast<int>(cols);
+    p.d = static_cast<int>(d);
+    p.mt = static_cast<int>(ceil_div(M, FR));
+    p.ct = static_cast<int>(ceil_div(cols, FR));
+    p.tiles = fused_tiles(B, M, cols);
+    p.scale = std::fabs(scale);
+    p.idesc_s = km::mma_idesc_f16(bf16 ? 1u : 0u, FR, FR) | (scale < 0.f ? 1u << 13 : 0u);   // bit 13 negates A
+    p.idesc_o = km::mma_idesc_f16(bf16 ? 1u : 0u, FR, DN) | (1u << 16);                      // B MN-major
+    p.points = w.points;
+    p.wmax = w.wmax;
+    p.pscale = pscale;
+    p.parts = w.parts;
+    p.out = out;
+    p.vec = d % 8 == 0 && aligned(out, 16) ? 1 : 0;
+    const int blocks = fused_blocks(p.tiles);
+    kernel<<<blocks, F_THREADS, Sh::kTotal, st>>>(tmA, tmB, p);
+    if (launch_status() != KM_OK || blocks == 1) return launch_status();
+    // (nothing to join where the blocks' shares are whole row tiles)
+    if (p.tiles % blocks == 0 && p.tiles / blocks % p.ct == 0) return KM_OK;
+    const int rows = p.tiles / p.ct;
+    auto join = [&](auto parts, int units) {
+        constexpr int PARTS = decltype(parts)::value;
+        fused_join_kernel<T, DN, PARTS><<<static_cast<unsigned>(units) * (FR * PARTS / 4), DN, 0, st>>>(
+            w.parts, p.tiles, blocks, p.M, p.d, p.mt, p.ct, w.wmax, pscale, static_cast<T *>(out));
+    };
+    // (from 16 blocks to a row tile on, its partials are worth sharing out)
+    if (blocks >= 16 * rows) join(std::integral_constant<int, 4>(), rows);
+    else join(std::integral_constant<int, 1>(), blocks - 1);
+    return launch_status();
+}
+
+template <typename T>
+km_status fused_grads(const void *X, km_dtype dt, const void *C, const int32_t *ids, const float *lse, const float *g,
+                      int64_t B, int64_t N, int64_t K, int64_t d, float scale, void *dX, void *dC, void *ws,
+                      cudaStream_t st) {
+    if (!encode_fn()) return KM_ERR_CUDA;
+    Carver cv(ws);
+    const FusedWs w = carve_fused(cv, B, N, K, d, dt);
+    const int64_t dp = padded(d, dt);
+    const float pscale = dt == KM_F16 ? 16384.f : 1.f;
+    km_status s;
+    if (cudaMemsetAsync(w.wmax, 0, 4, st) != cudaSuccess) return KM_ERR_CUDA;
+    km::xe::weight_kernel<<<static_cast<unsigned>(ceil_div(B * N, 256)), 256, 0, st>>>(
+        g, ids, B * N, static_cast<int>(K), scale, w.w, w.wmax);
+    if (launch_status() != KM_OK) return KM_ERR_CUDA;
+    point_param_kernel<<<fill_blocks(B * w.ptiles * FR), 256, 0, st>>>(w.w, lse, ids, B, static_cast<int>(N), w.ptiles,
+                                                                static_cast<int>(K), w.wmax, pscale, w.points);
+    if (launch_status() != KM_OK) return KM_ERR_CUDA;
+    // points without a label become zeros, so that nothing they hold reaches a sum
+    if ((s = copy_rows<T>(X, ids, B * N, d, dp, K, w.X, st)) != KM_OK) return s;
+    X = w.X;
+    if (dp != d || !aligned(C, 16)) {
+        if ((s = copy_rows<T>(C, nullptr, B * K, d, dp, K, w.C, st)) != KM_OK) return s;
+        C = w.C;
+    }
+    if (dX) {
+        s = d > 64 ? fused_launch<T, 128, false>(X, C, B, N, K, d, dp, scale, w, pscale, dX, st)
+                   : fused_launch<T, 64, false>(X, C, B, N, K, d, dp, scale, w, pscale, dX, st);
+        if (s != KM_OK) return s;
+    }
+    if (dC) {
+        s = d > 64 ? fused_launch<T, 128, true>(C, X, B, K, N, d, dp, scale, w, pscale, dC, st)
+                   : fused_launch<T, 64, true>(C, X, B, K, N, d, dp, scale, w, pscale, dC, st);
+        if (s != KM_OK) return s;
+    }
+    return KM_OK;
+}
+
 template <typename T>
 km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *ids, const float *lse, const float *g,
                      int64_t B, int64_t N, int64_t K, int64_t d, float scale, void *dX, void *dC, void *ws,
                      cudaStream_t st) {
+    if constexpr (!std::is_same<T, float>::value)
+        if (fused_shape(dt, d)) return fused_grads<T>(X, dt, C, ids, lse, g, B, N, K, d, scale, dX, dC, ws, st);
     Carver cv(ws);
     const GradWs w = carve_grad(cv, B, N, K, d, dt);
     const bool tc = use_tc(dt, d, scale, X, C);
@@ -403,7 +519,8 @@ km_status km_xent(const void *X, km_dtype dtype, const void *C, const int32_t *i
 size_t km_xent_grad_workspace_size(int64_t B, int64_t N, int64_t K, int64_t d, km_dtype dtype) {
     if (!valid_dtype(dtype) || !xent_sizes_ok(B, N, K, d)) return 0;
     Carver c(nullptr);
-    carve_grad(c, B, N, K, d, dtype);
+    if (fused_shape(dtype, d)) carve_fused(c, B, N, K, d, dtype);
+    else carve_grad(c, B, N, K, d, dtype);
     return c.off;
 }
 

@@ -1,5 +1,5 @@
 // km_xent_tc.cuh -- the products of the cross entropy and its gradients on the 5th-generation
-// tensor cores (tcgen05, TMEM, TMA), one SM pair per 256 x BN tile (cta_group::2).
+// tensor cores (tcgen05, TMEM, TMA), one SM pair per 256 x 256 tile (cta_group::2).
 //
 // One kernel forms D[m,n] = sum_k A(m,k) B(n,k) for the three products and differs in how the
 // operands lie in memory and in what becomes of a tile:
@@ -10,15 +10,16 @@
 // An operand whose reduction index is the contiguous one is staged K-major, the others MN-major,
 // so P, X and C are read as they lie and nothing is transposed in memory.
 //
-// Shared memory per CTA and stage of 64 reduction steps: 128 rows of A (16 KB) and BN / 2 of B;
-// both CTAs of a pair stage half of B, which the pair's MMAs share. The 512 TMEM columns hold two
+// Shared memory per CTA and stage of 64 reduction steps: 128 rows of A (16 KB) and of B;
+// each CTA of a pair stages half of B, which the pair's MMAs share. The 512 TMEM columns hold two
 // accumulators, so a tile's epilogue runs while the next tile is computed.
 //
 // Roles per CTA (12 warps): warp 0 requests the tiles; warp 1 of the leader issues the MMAs;
 // warps 4-11 are the epilogue (TMEM lane quarter = warp % 4, column half = (warp - 4) / 4, one row
-// per thread; sixteen warps with half the columns each were no faster). Waits are bounded like everywhere in the library: a role that gives up sets the
-// CTA's abort flag, the producer waits for the copies it asked for, the issuer for its MMAs, the
-// pair synchronises and frees TMEM. No TMA load uses multicast.
+// per thread; sixteen warps with half the columns each were no faster). Waits are bounded like
+// everywhere in the library: a role that gives up sets the CTA's abort flag, the producer waits for the
+// copies it asked for, the issuer for its MMAs, the pair synchronises and frees TMEM. No TMA load uses
+// multicast.
 #pragma once
 
 #include "km_assign_tc.cuh"
@@ -28,18 +29,19 @@ namespace km {
 namespace xe {
 
 constexpr int TBM = 128;                 // rows per CTA, 256 per pair
+constexpr int TBN = 256;                 // columns of a tile
 constexpr int TKC = 64;                  // reduction steps per stage (128 bytes of 16-bit values)
 constexpr int T_EPI0 = 4, T_EPI_WARPS = 8;
 constexpr int T_THREADS = 32 * (T_EPI0 + T_EPI_WARPS);
 constexpr uint32_t kOutBuf = 32 * 128;    // bytes of a P store
 constexpr int T_GROUP = 8;               // row tiles that share their column tiles in L2
 
-template <int BN, int MODE> struct TcShape {
-    static constexpr uint32_t kA = TBM * 128u, kB = (BN / 2) * 128u;
+template <int MODE> struct TcShape {
+    static constexpr uint32_t kA = TBM * 128u, kB = (TBN / 2) * 128u;
     static constexpr uint32_t kStage = kA + kB;
     // kProb: two 32-row x 64-column buffers per epilogue warp, from which P is stored by TMA
     static constexpr uint32_t kOutBytes = MODE == kProb ? T_EPI_WARPS * 2 * kOutBuf : 0;
-    static constexpr int kStages = BN == 256 ? (MODE == kProb ? 5 : 6) : 8;
+    static constexpr int kStages = MODE == kProb ? 5 : 6;
     static constexpr uint32_t kOutOff = kStages * kStage;
     static constexpr uint32_t kBarOff = kOutOff + kOutBytes;
     static constexpr int kBars = 2 * kStages + 5;
@@ -125,14 +127,14 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, f
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <typename T, int BN, int MODE, bool AMN, bool BMN>
+template <typename T, int MODE, bool AMN, bool BMN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
     tc_product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmP, const TcParams p, const Epi ep) {
-    using Sh = TcShape<BN, MODE>;
+    using Sh = TcShape<MODE>;
     using namespace km::tc;
     constexpr int S = Sh::kStages;
-    constexpr int HALF = BN / 2;             // columns per epilogue warp
+    constexpr int HALF = TBN / 2;             // columns per epilogue warp
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_flag;
     const uint32_t raw = smem_u32(smem_raw);
@@ -185,7 +187,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
         for (int t = t0; t < total && ok; t += tstep) {
             const TcItem it = tc_item(p, t);
             const int mrow = it.m * (2 * TBM) + static_cast<int>(rank) * TBM;
-            const int nrow = it.n * BN + static_cast<int>(rank) * (BN / 2);
+            const int nrow = it.n * TBN + static_cast<int>(rank) * (TBN / 2);
             const int kc1 = min(p.kchunks, (it.split + 1) * p.kper);
             for (int kc = it.split * p.kper; kc < kc1; ++kc) {
                 if (!mbar_wait_warp(EMPTY(stage), ph ^ 1u, abortp)) { ok = false; break; }
@@ -202,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                     }
                     if (BMN) {
 #pragma unroll
-                        for (int i = 0; i < BN / 128; ++i)
+                        for (int i = 0; i < TBN / 128; ++i)
                             tma_load_3d_pair(bsm + i * 8192, &tmB, bar, nrow + i * 64, kc * TKC, it.b, pol);
                     } else {
                         tma_load_3d_pair(bsm, &tmB, bar, kc * TKC, nrow, it.b, pol);
@@ -296,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
         for (int t = t0; t < total; t += tstep) {
             const TcItem it = next;
             const int row0 = it.m * (2 * TBM) + static_cast<int>(rank) * TBM + q * 32, row = row0 + lane;
-            const int c0 = it.n * BN + half * HALF;
+            const int c0 = it.n * TBN + half * HALF;
             const bool rin = row < p.M;
             const int64_t br = static_cast<int64_t>(it.b) * p.M + row;
             int label = -1;

@@ -26,7 +26,8 @@ pytestmark = pytest.mark.gpu
 DTYPES = [torch.float16, torch.bfloat16, torch.float32]
 SHAPES = [(1, 1, 1, 1), (1, 1, 2, 8), (2, 3, 5, 7), (1, 128, 128, 64), (1, 129, 257, 128), (3, 50, 300, 24),
           (1, 300, 1000, 136), (2, 257, 130, 72), (1, 5, 4099, 33), (1, 1000, 3, 16), (4, 64, 64, 512),
-          (1, 200, 520, 1000), (1, 70, 2100, 256)]
+          (1, 200, 520, 1000), (1, 70, 2100, 256), (1, 1, 5000, 64), (1, 2000, 1, 100),
+          (2, 384, 640, 128), (3, 129, 385, 65), (1, 40, 1500, 129)]
 
 
 def _inputs(B, N, K, d, dtype, dev, seed, scale_rows=2.0):
@@ -108,10 +109,12 @@ def test_xent_and_gradients(cuda_device, dtype, B, N, K, d):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_many_pieces_and_split_reductions(cuda_device, dtype):
-    # a table of several gradient pieces (the scratch holds 2^27 entries of P at a time) and a
-    # reduction over many points; checked on a sample of rows through fp64 torch on the device
-    B, N, K, d = 1, 65536, 5000, 40
+@pytest.mark.parametrize("d", [40, 136])
+def test_many_pieces_and_split_reductions(cuda_device, dtype, d):
+    # a table of several gradient pieces (the scratch holds 2^27 entries of P at a time; rows of up
+    # to 128 16-bit values need none) and a reduction over many points; checked through fp64 torch
+    # on the device
+    B, N, K = 1, 65536, 5000
     X, C, ids, g = _inputs(B, N, K, d, dtype, cuda_device, seed=1)
     loss, lse = km.km_xent(X, C, ids)
     dX, dC = km.km_xent_grad(X, C, ids, lse, g)
