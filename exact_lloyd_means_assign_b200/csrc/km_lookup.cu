@@ -42,9 +42,8 @@ constexpr int kLookupThreads = 256;
 
 // A warp serves `rpw` consecutive rows (at most 32): each lane finds one row's source once, then
 // the rows are moved 32 / TPR at a time, TPR lanes (a power of two) per row and V elements per lane,
-// with 2 rows (4 pieces of a wide row) in flight
-// per lane: more registers per thread cost more in resident warps than they hide (8: 122 us, 4: 91,
-// 2: 87 for 2M rows of 256 bytes). Off is the type of offsets counted in units of V elements: 32 bits
+// with 2 rows (4 pieces of a wide row) in flight per lane: more registers per thread cost more in
+// resident warps than they hide (8: 122 us, 4: 91, 2: 87 for 2M rows of 256 bytes, 6.3 TB/s). Off is the type of offsets counted in units of V elements: 32 bits
 // wherever table and output have fewer units than 2^32, which halves the address arithmetic that
 // otherwise costs more than the conversion of the values.
 template <typename T, int V, int TPR, typename Off>
@@ -238,34 +237,36 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// Stable ranks of a warp's entries among equal digits: entry i of a lane is number i * 32 + lane of
-// the warp's. The lanes with an equal digit are found by a ballot per digit bit (a warp match has a
-// far lower rate), for all entries first: the ballots do not depend on one another, the counting
-// that follows does. mine[bin] counts the warp's entries.
-__device__ __forceinline__ void rank_digits(const uint32_t (&digit)[kSortItems], const bool (&ok)[kSortItems], int per,
-                                            uint16_t *mine, uint16_t (&rank)[kSortItems]) {
-    const int lane = threadIdx.x & 31;
-    uint32_t peers[kSortItems];
+// Stable ranks of a warp's entries among equal digits: entry i of a lane (there if bit i of ok is set) is
+// number i * 32 + lane of the warp's. The lanes with an equal digit are found by a ballot per digit bit
+// (a warp match has a far lower rate), for all entries first: the ballots do not depend on one another,
+// the counting that follows does. mine[bin] counts the warp's entries.
+template <typename Digit>
+__device__ __forceinline__ void rank_digits(const Digit &digit, uint32_t ok, int per, uint16_t *mine, uint32_t (&rank)[kSortItems]) {
+    const uint32_t below = (1u << (threadIdx.x & 31)) - 1;
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
         if (i >= per) break;
-        uint32_t p = __ballot_sync(0xffffffffu, ok[i]);
+        const uint32_t d = digit(i);
+        uint32_t p = __ballot_sync(0xffffffffu, (ok >> i) & 1);
 #pragma unroll
         for (int b = 0; b < kMaxWidth; ++b) {
-            const bool bit = (digit[i] >> b) & 1;
+            const bool bit = (d >> b) & 1;
             const uint32_t v = __ballot_sync(0xffffffffu, bit);
             p &= bit ? v : ~v;
         }
-        peers[i] = p;
+        rank[i] = __popc(p & below) | __popc(p) << 8;       // equal digits in lower lanes, in all
     }
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
         if (i >= per) break;
+        const bool has = (ok >> i) & 1;
+        const uint32_t d = digit(i), lower = rank[i] & 255, all = rank[i] >> 8;
         uint32_t prior = 0;
-        if (ok[i]) prior = mine[digit[i]];
+        if (has) prior = mine[d];
         __syncwarp();
-        rank[i] = static_cast<uint16_t>(prior + __popc(peers[i] & ((1u << lane) - 1)));
-        if (ok[i] && lane == __ffs(peers[i]) - 1) mine[digit[i]] = static_cast<uint16_t>(prior + __popc(peers[i]));
+        rank[i] = prior + lower;
+        if (has && lower == 0) mine[d] = static_cast<uint16_t>(prior + all);
         __syncwarp();
     }
 }
@@ -300,7 +301,9 @@ __device__ __forceinline__ void block_scan_bins(uint32_t (&v)[2], uint32_t *ws, 
 
 // Sorts a tile by the pass's digit in shared memory and writes its runs to (start of the bin) +
 // (entries of the bin in earlier tiles): consecutive threads write consecutive entries of a run.
-__global__ void __launch_bounds__(kSortThreads)
+// Two blocks to an SM (64 registers, some spilled) hide more of the chain load, rank, scan, store than one
+// with all it asks for: gradient of 1024 rows x 32 batches over 65536 tokens each 172 to 165 us.
+__global__ void __launch_bounds__(kSortThreads, 2)
     sort_scatter_kernel(const SortSpec s, const uint32_t *__restrict__ counts, const uint32_t *__restrict__ totals,
                         uint32_t *__restrict__ keys_out, uint32_t *__restrict__ pos_out) {
     extern __shared__ uint32_t dyn[];
@@ -312,14 +315,10 @@ __global__ void __launch_bounds__(kSortThreads)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nb = 1 << s.width;
     const uint32_t seg = blockIdx.x / s.tps, tile = blockIdx.x - seg * s.tps;
     const uint32_t i0 = warp * (32 * kSortItems) + lane;
-    uint32_t key[kSortItems], digit[kSortItems], pos;
-    uint16_t rank[kSortItems];
-    bool ok[kSortItems];
+    uint32_t key[kSortItems], rank[kSortItems], pos, ok = 0;
 #pragma unroll
-    for (int i = 0; i < kSortItems; ++i) {
-        ok[i] = sort_load(s, seg, tile * kSortTile + i0 + i * 32, key[i], pos);
-        digit[i] = ok[i] ? sort_digit(s, seg, key[i]) : 0;
-    }
+    for (int i = 0; i < kSortItems; ++i) ok |= static_cast<uint32_t>(sort_load(s, seg, tile * kSortTile + i0 + i * 32, key[i], pos)) << i;
+    auto digit = [&](int i) { return sort_digit(s, seg, key[i]); };
     for (int k = threadIdx.x; k < kSortWarps * nb / 2; k += kSortThreads) reinterpret_cast<uint32_t *>(wcount)[k] = 0;
     // valid tokens of earlier segments
     uint32_t before = 0, all = 0;
@@ -373,8 +372,8 @@ __global__ void __launch_bounds__(kSortThreads)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i)
-        if (ok[i]) {
-            const uint32_t at = mine[digit[i]] + rank[i];
+        if ((ok >> i) & 1) {
+            const uint32_t at = mine[digit(i)] + rank[i];
             skeys[at] = key[i];
             sloc[at] = static_cast<uint16_t>(i0 + i * 32);
         }
@@ -457,16 +456,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads,
     const uint32_t E = static_cast<uint32_t>(per) * kSortThreads, e0 = rank_c * E;
     const FastDiv div_e = s.divE;
     const uint32_t i0 = static_cast<uint32_t>(warp * 32 * per + lane);
-    uint32_t key[kSortItems], pos[kSortItems], digit[kSortItems];
-    uint16_t rank[kSortItems];
-    bool ok[kSortItems];
-    uint32_t valid = 0;
+    uint32_t key[kSortItems], pos[kSortItems];
+    uint32_t rank[kSortItems], ok = 0, valid = 0;
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
         const uint32_t at = e0 + i0 + i * 32;
-        ok[i] = i < per && at < tokens;
         pos[i] = at;
-        if (ok[i]) {
+        if (i < per && at < tokens) {
+            ok |= 1u << i;
             const uint32_t id = static_cast<uint32_t>(s.ids[at]);
             key[i] = id < s.K ? fd_div(s.divN, at) * s.K + id : keys_total;
             valid += id < s.K;
@@ -479,8 +476,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads,
     for (int pass = 0; pass < passes; ++pass) {
         for (int k = threadIdx.x; k < kSortWarps * nb / 2; k += kSortThreads) reinterpret_cast<uint32_t *>(wcount)[k] = 0;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kSortItems; ++i) digit[i] = ok[i] ? (key[i] >> (pass * s.width)) & (nb - 1) : 0;
+        auto digit = [&](int i) { return (key[i] >> (pass * s.width)) & (nb - 1); };
         rank_digits(digit, ok, per, mine, rank);
         __syncthreads();
         for (int b = threadIdx.x; b < nb; b += kSortThreads) bincount[b] = sum_warps(wcount, nb, b);
@@ -524,8 +520,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads,
         const bool final = pass + 1 == passes;
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i)
-            if (ok[i]) {
-                const uint32_t at = bincount[digit[i]] + mine[digit[i]] + rank[i];
+            if ((ok >> i) & 1) {
+                const uint32_t at = bincount[digit(i)] + mine[digit(i)] + rank[i];
                 if (final) {
                     keys_out[at] = key[i];
                     pos_out[at] = pos[i];
@@ -538,7 +534,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads,
         if (final) break;
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i)
-            if (ok[i]) {
+            if ((ok >> i) & 1) {
                 const uint2 v = entries[i0 + i * 32];
                 key[i] = v.x;
                 pos[i] = v.y;
@@ -629,6 +625,9 @@ __device__ __forceinline__ uint32_t range_begin(const uint32_t *keys, uint32_t n
 // one after the other in fp32; a whole run goes to its table row, a cut one to the range's slots,
 // and the range that a cut run begins in enters the run into the list of joins. SHORT: a range's
 // possible entries are at most LPR, read in one go together with the search for its ends.
+// Bound by memory: each row of dY is read once, in whole rows but in the order of the ids. 2M rows of 256
+// bytes into 32 x 1024 rows: 112 us for 548 MB read, 4.9 TB/s (a plain copy moves 6.5); 8192 rows of 4 KB
+// into 32000: 20 us under the profiler, short runs' latency and the zeros' writing before it.
 template <typename T, typename O, int V, int LPR, bool SHORT>
 __global__ void __launch_bounds__(kGradThreads)
     grad_ranges_kernel(const T *__restrict__ dY, const GradParams p, O *__restrict__ dC) {
