@@ -8,7 +8,8 @@
 // The N x K logits are never stored. The loss reduces every tile of logits to one (maximum, sum of
 // exponentials) pair per row where the tile was computed, the same idea as the assignment's
 // running argmin, and joins the pairs of a row afterwards in tile order. The gradients recompute
-// the logits one piece of the table at a time into P (in the points' type) and multiply that.
+// the logits one piece of the table at a time into P (in the points' type) and multiply that; 16-bit rows
+// of up to 128 values keep P on the chip instead (km_xent_fused.cuh).
 #pragma once
 
 #include "km_common.cuh"

@@ -421,7 +421,7 @@ km_status km_lookup(const void *C, km_dtype dtype, const int32_t *ids, int64_t B
  * rows of dY not read. Without accumulate, rows without tokens are set to zero; with it they are
  * left as they are. dY[B,N,d] in `dtype`; dC[B,K,d] in `out_dtype`, which is `dtype` or fp32.
  * ws: km_lookup_grad_workspace_size(...) bytes, 256-byte aligned (0 is returned for sizes that
- * are not provided). Asynchronous on `stream`. Errors: KM_ERR_INVALID_ARG; KM_ERR_UNSUPPORTED
+ * are not provided); calls that may overlap need a workspace each. Asynchronous on `stream`. Errors: KM_ERR_INVALID_ARG; KM_ERR_UNSUPPORTED
  * (B*N or B*K of 2^31 or more, other out_dtype); KM_ERR_WORKSPACE; KM_ERR_CUDA.
  */
 size_t km_lookup_grad_workspace_size(int64_t B, int64_t N, int64_t K, int64_t d);
@@ -440,13 +440,16 @@ km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int
  * without a label,
  *     dX[b,n] = sum_k P[n,k] C[b,k],      dC[b,k] = sum_n P[n,k] X[b,n].
  * lse as km_xent wrote it; g[B,N] fp32, the gradient of each loss, NULL = all ones; dX[B,N,d],
- * dC[B,K,d] in `dtype`, either may be NULL. The logits are computed again, one piece of the table
- * at a time, and P is held in `dtype`, relative to the largest |g * scale| (fp16: times 2^14, so
- * that small probabilities keep their bits); all sums are fp32, in an order fixed by the sizes. Points without a label may hold any values: they reach
- * neither gradient (their own rows of dX are zero).
+ * dC[B,K,d] in `dtype`, either may be NULL; they may not overlap the inputs. The logits are computed
+ * again (16-bit rows of up to 128 values: tile by tile for each gradient, without scratch for P; else
+ * one piece of the table at a time), and P is held in `dtype`, relative to the largest |g * scale|
+ * (fp16: times 2^14, so that small probabilities keep their bits); all sums are fp32, in an order fixed
+ * by the sizes and the number of SMs. Points without a label may hold any values: they reach neither
+ * gradient (their own rows of dX are zero).
  *
  * ws: km_xent_workspace_size / km_xent_grad_workspace_size bytes, 256-byte aligned (0 for sizes
- * that are not provided). Asynchronous on `stream`. Errors: KM_ERR_INVALID_ARG;
+ * that are not provided; asked for with the device of the call current). Calls that may overlap need
+ * a workspace each. Asynchronous on `stream`. Errors: KM_ERR_INVALID_ARG;
  * KM_ERR_UNSUPPORTED (B*N, or B * ceil(N/128) * ceil(K/128), of 2^31 or more);
  * KM_ERR_WORKSPACE; KM_ERR_CUDA.
  */

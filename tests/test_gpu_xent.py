@@ -8,8 +8,7 @@ exponentials is positive and at most 256 + tiles additions deep. Hence
   e_lse  = max e_z + 2^-21 (max |z| + 2) + (320 + K / 64) 2^-24,
   e_loss = e_lse + e_z(label).
 P carries the relative error e_z + e_lse + 2^-21 (max |z| + 2) on its probability part and is rounded
-to its type, half a step u (fp16: P is scaled by a power of two f with |w| f < 2^15 and max |w| f >=
-2^14, so its absolute floor is half a subnormal step, 2^-25 2^-14 max |w|):
+to its type, half a step u (fp16: P is scaled by f with max |w| f = 2^14, so its absolute floor is half a subnormal step, 2^-25 2^-14 max |w|):
   e_P = |w| (p (e_z + e_lse + ...) + u |p - [label]|) + floor.
 The products with C and X then give e_P |C| + depth 2^-23 |P| |C| + half a step of the result.
 """
@@ -27,7 +26,7 @@ DTYPES = [torch.float16, torch.bfloat16, torch.float32]
 SHAPES = [(1, 1, 1, 1), (1, 1, 2, 8), (2, 3, 5, 7), (1, 128, 128, 64), (1, 129, 257, 128), (3, 50, 300, 24),
           (1, 300, 1000, 136), (2, 257, 130, 72), (1, 5, 4099, 33), (1, 1000, 3, 16), (4, 64, 64, 512),
           (1, 200, 520, 1000), (1, 70, 2100, 256), (1, 1, 5000, 64), (1, 2000, 1, 100),
-          (2, 384, 640, 128), (3, 129, 385, 65), (1, 40, 1500, 129)]
+          (2, 384, 640, 128), (3, 129, 385, 65), (1, 40, 1500, 129), (1, 6000, 40, 128), (1, 9, 6000, 72)]
 
 
 def _inputs(B, N, K, d, dtype, dev, seed, scale_rows=2.0):
