@@ -626,8 +626,8 @@ __device__ __forceinline__ uint32_t range_begin(const uint32_t *keys, uint32_t n
 // and the range that a cut run begins in enters the run into the list of joins. SHORT: a range's
 // possible entries are at most LPR, read in one go together with the search for its ends.
 // Bound by memory: each row of dY is read once, in whole rows but in the order of the ids. 2M rows of 256
-// bytes into 32 x 1024 rows: 112 us for 548 MB read, 4.9 TB/s (a plain copy moves 6.5); 8192 rows of 4 KB
-// into 32000: 20 us under the profiler, short runs' latency and the zeros' writing before it.
+// bytes into 32 x 1024 rows: 112 us for 548 MB read, 4.9 TB/s (a plain copy moves 6.5). 16384 rows of
+// 2 KB into 65536: 21 us under the profiler for 33 MB, the latency of short runs.
 template <typename T, typename O, int V, int LPR, bool SHORT>
 __global__ void __launch_bounds__(kGradThreads)
     grad_ranges_kernel(const T *__restrict__ dY, const GradParams p, O *__restrict__ dC) {
