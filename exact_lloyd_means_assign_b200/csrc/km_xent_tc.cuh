@@ -12,8 +12,9 @@
 //
 // Bound by the tensor pipe: 8192 points x 32768 rows at d = 1024, bf16: the logits 339 us (1.62
 // PFLOP/s, the pipe 94 % busy); with the gradients 1524 us: P at 81 % of the pipe, the products with it at
-// 77 and 73, their 128 and 256 tiles leaving part of the last wave of 74 pairs empty. At d = 128 the
-// exponentials bound the logits: 32768 x 8192 122 us, the special-function pipe 57 % busy.
+// 77 and 73, their 128 and 256 tiles leaving part of the last wave of 74 pairs empty. At d = 128
+// the epilogue bounds the logits: 32768 x 8192 116 us, the special-function pipe some 60 % busy (moving a
+// quarter of the exponentials to the FMA pipe did not help).
 //
 // Shared memory per CTA and stage of 64 reduction steps: 128 rows of A (16 KB) and of B;
 // each CTA of a pair stages half of B, which the pair's MMAs share. The 512 TMEM columns hold two
@@ -112,6 +113,9 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, f
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+
+__device__ __forceinline__ void ld_cols(uint32_t a, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(a, v); }
+__device__ __forceinline__ void ld_cols(uint32_t a, uint32_t (&v)[64]) { tmem_ld_32x32b_x64(a, v); }
 
 template <typename T, int MODE, bool AMN, bool BMN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
@@ -307,36 +311,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
             tc_fence_after();
             float m = 0.f;
             uint64_t s4[4] = {0, 0, 0, 0};
-            // columns in chunks of 32, the next chunk's load in flight while one is worked on
-            uint32_t v2[2][32];
-            tmem_ld_32x32b_x32(tl + buf * ACC_STRIDE, v2[0]);
+            // columns in chunks of 32, 64 for the loss (fewer corrections of the sums by a new maximum: 32768 x
+            // 8192 at d = 128 122 to 116 us), the next chunk's load in flight while one is worked on
+            constexpr int CH = MODE == kLse ? 64 : 32;
+            uint32_t v2[2][CH];
+            ld_cols(tl + buf * ACC_STRIDE, v2[0]);
 #pragma unroll
-            for (int ch = 0; ch < HALF / 32; ++ch) {
-                uint32_t(&v)[32] = v2[ch & 1];
+            for (int ch = 0; ch < HALF / CH; ++ch) {
+                uint32_t(&v)[CH] = v2[ch & 1];
                 tmem_wait_ld(v);
-                if (ch + 1 < HALF / 32) {
-                    tmem_ld_32x32b_x32(tl + buf * ACC_STRIDE + (ch + 1) * 32, v2[(ch + 1) & 1]);
+                if (ch + 1 < HALF / CH) {
+                    ld_cols(tl + buf * ACC_STRIDE + (ch + 1) * CH, v2[(ch + 1) & 1]);
                 } else {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(buf ? empty1 : empty0);
                 }
-                const int col = c0 + ch * 32;
+                const int col = c0 + ch * CH;
                 if (MODE == kLse) {
                     if (col < p.N) {
-                        if (col + 32 > p.N) {
+                        if (col + CH > p.N) {
                             asm volatile("");      // a branch: this is the table's last tile only
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < CH; ++i)
                                 if (col + i >= p.N) v[i] = 0xff800000u;      // -inf
                         }
                         float cm = __uint_as_float(v[0]), cm2 = __uint_as_float(v[1]);
 #pragma unroll
-                        for (int i = 2; i < 30; i += 4) {
+                        for (int i = 2; i < CH - 2; i += 4) {
                             cm = max3f(cm, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
                             cm2 = max3f(cm2, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                         }
-                        cm = max3f(max3f(cm, __uint_as_float(v[30]), __uint_as_float(v[31])), cm2, cm);
+                        cm = max3f(max3f(cm, __uint_as_float(v[CH - 2]), __uint_as_float(v[CH - 1])), cm2, cm);
                         const float nm = ch ? fmaxf(m, cm) : cm;
                         if (ch) {
                             const float corr = ex2f((m - nm) * s2);
@@ -348,16 +354,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                         const float d = -nm * s2;
                         const uint64_t d2 = pair_f32(d, d);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int i = 0; i < CH; i += 2) {
                             float a, b;
                             unpair_f32(fma2(pair_f32(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s22, d2), a, b);
                             s4[(i >> 1) & 3] = add2(s4[(i >> 1) & 3], pair_f32(ex2f(a), ex2f(b)));
                         }
-                        if (label >= col && label < col + 32) {
+                        if (label >= col && label < col + CH) {
                             asm volatile("");
                             float zt = 0.f;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < CH; ++i)
                                 if (col + i == label) zt = __uint_as_float(v[i]) * sc;
                             ep.zt[br] = zt;
                         }
