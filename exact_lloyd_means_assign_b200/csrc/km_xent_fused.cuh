@@ -55,6 +55,12 @@ template <int DN, bool COL> struct FShape {
     static constexpr int kBars = 2 * kStages + 13;
     static constexpr uint32_t kTotal = kBarOff + kBars * 8 + 16 + 1024;
 };
+template <typename T> __device__ __forceinline__ float unpack_lo(uint32_t v) {
+    const uint16_t h = static_cast<uint16_t>(v);
+    return Cvt<T>::to_f(*reinterpret_cast<const T *>(&h));
+}
+template <typename T> __device__ __forceinline__ float unpack_hi(uint32_t v) { return unpack_lo<T>(v >> 16); }
+
 constexpr int F_SBUFS = 3;
 constexpr uint32_t F_OCOL = F_SBUFS * FR;          // TMEM: S and P, then O
 
@@ -138,8 +144,11 @@ __device__ __forceinline__ void label_entry(const uint32_t (&v)[32], uint32_t (&
         o[i] = __byte_perm(o[i], e16, i == k >> 1 ? sel : 0x3210);
 }
 
-// COL: the points are the columns of P (dC), else the rows (dX).
-template <typename T, int DN, bool COL>
+// COL: the points are the columns of P (dC), else the rows (dX). LO: P in two 16-bit parts, the second
+// what the first's rounding left: with few table rows (128 at most) an entry is a large share of its
+// row's sum, and its rounding, which a sum over many entries averages away, would be as large as the result's own.
+// In TMEM the parts of 32 columns lie side by side where their S was.
+template <typename T, int DN, bool COL, bool LO>
 __global__ void __launch_bounds__(F_THREADS, 1)
     fused_grad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const FParams p) {
     using Sh = FShape<DN, COL>;
@@ -256,7 +265,12 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                     f_mma_ts(tmem + F_OCOL, po, bd, kDescHi, p.idesc_o, first ? 0u : 1u);
 #pragma unroll
                     for (int kk = 1; kk < FR / 16; ++kk)
-                        f_mma_ts(tmem + F_OCOL, po + kk * 8, bd + kk * (2048 >> 4), kDescHi, p.idesc_o, 1u);
+                        f_mma_ts(tmem + F_OCOL, po + (kk >> 1) * 32 + (kk & 1) * 8, bd + kk * (2048 >> 4), kDescHi, p.idesc_o, 1u);
+                    if (LO) {
+#pragma unroll
+                        for (int kk = 0; kk < FR / 16; ++kk)
+                            f_mma_ts(tmem + F_OCOL, po + 16 + (kk >> 1) * 32 + (kk & 1) * 8, bd + kk * (2048 >> 4), kDescHi, p.idesc_o, 1u);
+                    }
                     // (the group has read the tile's parameters before it gave P)
                     tc_commit(B_EMPTY(slot_o));
                     if (last) {
@@ -346,7 +360,34 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                     tmem_ld_32x32b_x32(ts + c * 32, v);
                     tmem_wait_ld(v);
                     const int col0 = j * FR + c * 32;           // B's row of the first column
-                    if constexpr (!COL) {
+                    if constexpr (LO) {
+                        uint32_t rest[16];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            float e[2];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float off_k = off, w_k = w;
+                                bool mine = col0 + k + h == label;
+                                if (COL) {
+                                    const uint32_t at = pp + (c * 32 + k + h) * 4;
+                                    int l;
+                                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(off_k) : "r"(at));
+                                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w_k) : "r"(at + FR * 4));
+                                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(l) : "r"(at + FR * 8));
+                                    mine = l == grow;
+                                }
+                                e[h] = ex2f(fmaf(__uint_as_float(v[k + h]), s2, off_k));
+                                if (mine) e[h] -= fabsf(w_k);
+                                if (w_k < 0.f) e[h] = -e[h];
+                                if (!COL && col0 + k + h >= p.cols) e[h] = 0.f;
+                            }
+                            const uint32_t hi = pack2<T>(e[0], e[1]);
+                            o[k >> 1] = hi;
+                            rest[k >> 1] = pack2<T>(e[0] - unpack_lo<T>(hi), e[1] - unpack_hi<T>(hi));
+                        }
+                        tmem_st_x16(ts + c * 32 + 16, rest);
+                    } else if constexpr (!COL) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             float x, y;
@@ -411,7 +452,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                             }
                         }
                     }
-                    tmem_st_x16(ts + c * 16, o);
+                    tmem_st_x16(ts + c * 32, o);
                 }
                 tmem_wait_st();
                 tc_fence_before();

@@ -63,7 +63,7 @@ def _check_loss(X, C, ids, scale, loss, lse):
     assert (got[bad] == 0).all()
 
 
-def _check_grad(X, C, ids, g, scale, dX, dC):
+def _check_grad(X, C, ids, g, scale, dX, dC, parts=1):
     dtype = X.dtype
     X64, C64, i, rl, rs, z, ez, eexp, elses = _errors(X, C, ids, scale)
     g64 = np.ones(i.shape) if g is None else g.cpu().double().numpy()
@@ -71,7 +71,8 @@ def _check_grad(X, C, ids, g, scale, dX, dC):
     u = torch.finfo(dtype).eps / 2
     aw = np.abs(w)[..., None]
     onehot = np.where(aw > 0, np.abs(P) / np.maximum(aw, 1e-300), 0.0)      # |p - onehot|
-    eP = aw * (p * (ez + (elses + eexp + 2.0 ** -23 * np.abs(rs))[..., None]) * 1.01 + (u + 2.0 ** -22) * onehot)
+    # (two parts: the second is the exact remainder of the first, half a step of it is lost)
+    eP = aw * (p * (ez + (elses + eexp + 2.0 ** -23 * np.abs(rs))[..., None]) * 1.01 + (u ** parts + 2.0 ** -22) * onehot)
     if dtype == torch.float16:
         eP += 2.0 ** -39 * np.abs(w).max() * (aw > 0)
     aC, aX, aP = np.abs(C64), np.abs(X64), np.abs(P)
@@ -105,6 +106,16 @@ def test_xent_and_gradients(cuda_device, dtype, B, N, K, d):
         aX, aC = km.km_xent_grad(X, C, ids, lse, gr, scale)
         assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
         assert torch.equal(aX, dX) and torch.equal(aC, dC)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("B,N,K,d", [(1, 400, 2, 64), (2, 150, 5, 128), (1, 300, 60, 33), (1, 200, 128, 100)])
+def test_few_table_rows_keep_two_parts_of_p(cuda_device, dtype, B, N, K, d):
+    X, C, ids, g = _inputs(B, N, K, d, dtype, cuda_device, seed=7 * N + K)
+    for scale, gr in ((0.25, None), (-0.5, g)):
+        loss, lse = km.km_xent(X, C, ids, scale)
+        dX, dC = km.km_xent_grad(X, C, ids, lse, gr, scale)
+        _check_grad(X, C, ids, gr, scale, dX, dC, parts=2)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
