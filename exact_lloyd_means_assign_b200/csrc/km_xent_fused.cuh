@@ -24,7 +24,8 @@
 // Roles (10 warps): 0 requests, 1 issues the MMAs, 2-9 take the exponentials: two groups of four warps,
 // even and odd tiles, so that one group's loads and stores lie under the other's exponentials; a thread
 // takes a row of 128. TMEM: three buffers of S, in which P replaces what has been read, and one of O. The
-// MMAs of O of tile i, once complete, are followed by those of S of tile i + 3 in the same buffer. Waits are bounded as everywhere in the library.
+// MMAs of O of tile i, once complete, are followed by those of S of tile i + 3 in the same buffer. Waits
+// are bounded as everywhere in the library.
 #pragma once
 
 #include "km_xent.cuh"
