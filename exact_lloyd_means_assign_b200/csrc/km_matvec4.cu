@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             }
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
+                __syncwarp();        // lanes without a token read none; the products want the whole warp
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     uint32_t f[4];
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) load_x<T, XV>(xr[n] + h * 32, 0, xin[n] ? p.N - at : 0, xt[n]);
                 const uint32_t wa = lds32(src ^ (h * 16)), wb = lds32((src ^ (h * 16)) + 8 * 128);
+                __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     uint32_t f[4];

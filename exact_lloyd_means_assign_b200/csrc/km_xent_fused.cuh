@@ -387,6 +387,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                             o[k >> 1] = hi;
                             rest[k >> 1] = pack2<T>(e[0] - unpack_lo<T>(hi), e[1] - unpack_hi<T>(hi));
                         }
+                        __syncwarp();
                         tmem_st_x16(ts + c * 32 + 16, rest);
                     } else if constexpr (!COL) {
 #pragma unroll
@@ -453,6 +454,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                             }
                         }
                     }
+                    __syncwarp();       // lanes part at a label; the store wants the whole warp
                     tmem_st_x16(ts + c * 32, o);
                 }
                 tmem_wait_st();

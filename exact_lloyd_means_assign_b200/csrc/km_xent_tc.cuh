@@ -319,6 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
 #pragma unroll
             for (int ch = 0; ch < HALF / CH; ++ch) {
                 uint32_t(&v)[CH] = v2[ch & 1];
+                __syncwarp();        // lanes part in a chunk's work; these instructions want the whole warp
                 tmem_wait_ld(v);
                 if (ch + 1 < HALF / CH) {
                     ld_cols(tl + buf * ACC_STRIDE + (ch + 1) * CH, v2[(ch + 1) & 1]);
