@@ -348,7 +348,8 @@ km_status fused_launch(const void *A, const void *Bo, int64_t B, int64_t M, int6
     p.vec = d % 8 == 0 && aligned(out, 16) ? 1 : 0;
     const int blocks = fused_blocks(p.tiles);
     kernel<<<blocks, F_THREADS, Sh::kTotal, st>>>(tmA, tmB, p);
-    if (launch_status() != KM_OK || blocks == 1) return launch_status();
+    const km_status launched = launch_status();      // (reading the error clears it)
+    if (launched != KM_OK || blocks == 1) return launched;
     // (nothing to join where the blocks' shares are whole row tiles)
     if (p.tiles % blocks == 0 && p.tiles / blocks % p.ct == 0) return KM_OK;
     const int rows = p.tiles / p.ct;
