@@ -62,6 +62,14 @@ template <typename T> __device__ __forceinline__ float unpack_lo(uint32_t v) {
 }
 template <typename T> __device__ __forceinline__ float unpack_hi(uint32_t v) { return unpack_lo<T>(v >> 16); }
 
+// A product's additions into TMEM truncate, about 1e-7 of the sum each where all terms have one sign
+// (measured: 28000 of them 2.5e-3), so that a long sum would drift further than its result's own rounding.
+// After 1024 of them O is drained and the pieces are added in fp32, through the block's partials: 1e-4 at
+// most, less than half of fp16's half step. (32768 x 8192 at d = 128: no slower; 131072 x 8192: dX 502 to
+// 508 us, dC 548 to 572.)
+constexpr int kMaxChain = 1024;
+template <bool LO> constexpr int fused_run() { return kMaxChain / (LO ? 2 * (FR / 16) : FR / 16); }    // tiles
+
 constexpr int F_SBUFS = 3;
 constexpr uint32_t F_OCOL = F_SBUFS * FR;          // TMEM: S and P, then O
 
@@ -153,7 +161,7 @@ template <typename T, int DN, bool COL, bool LO>
 __global__ void __launch_bounds__(F_THREADS, 1)
     fused_grad_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const FParams p) {
     using Sh = FShape<DN, COL>;
-    constexpr int S = Sh::kStages;
+    constexpr int S = Sh::kStages, RUN = fused_run<LO>();
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_flag;
     const uint32_t raw = smem_u32(smem_raw);
@@ -252,14 +260,14 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             constexpr uint32_t kDescHi = 1024u >> 4 | 1u << 14 | 2u << 29;   // 8-row groups 1 KB apart, version 1, 128-byte swizzle
             const int n = t1 - t0;
             int js = t0 % p.ct, jo = js;          // column tiles of the next S and of the next O
-            int slot_s = 0, slot_o = 0, seg_s = 0, seg_o = 0;
+            int slot_s = 0, slot_o = 0, seg_s = 0, run_o = 0, in_run = 0;
             int bs = 0, bo = 0;                                     // their buffers
             uint32_t ph_s = 0, ph_o = 0, pho = 0;
             for (int i = -F_SBUFS; i < n; ++i) {
                 if (i >= 0) {
                     // O of tile i
-                    const bool first = i == 0 || jo == 0, last = jo + 1 == p.ct || i + 1 == n;
-                    if (!mbar_wait(P_FULL(bo), pho, abortp) || (first && !mbar_wait(O_EMPTY, (seg_o & 1) ^ 1u, abortp))) break;
+                    const bool first = in_run == 0, last = jo + 1 == p.ct || i + 1 == n || in_run + 1 == RUN;
+                    if (!mbar_wait(P_FULL(bo), pho, abortp) || (first && !mbar_wait(O_EMPTY, (run_o & 1) ^ 1u, abortp))) break;
                     tc_fence_after();
                     // MN-major: 64-value blocks 16 KB apart (leading offset), 8-row groups 1 KB apart
                     const uint32_t bd = ((FR * 128) >> 4) << 16 | (ring + slot_o * Sh::kStage) >> 4, po = tmem + bo * FR;
@@ -274,9 +282,11 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                     }
                     // (the group has read the tile's parameters before it gave P)
                     tc_commit(B_EMPTY(slot_o));
+                    ++in_run;
                     if (last) {
                         tc_commit(O_FULL);
-                        ++seg_o;
+                        ++run_o;
+                        in_run = 0;
                     }
                     if (++jo == p.ct) jo = 0;
                     if (++bo == F_SBUFS) { bo = 0; pho ^= 1u; }
@@ -318,15 +328,16 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         const float s2 = p.scale * kLog2e;
         const uint64_t s22 = pair_f32(s2, s2);
         const float inv = p_factor(p.wmax, p.pscale, true);
-        int slot = 0, seg = 0;
+        int slot = 0, run = 0;
         uint32_t ph = 0, sph = 0, odd = 0;          // phases; parity of the tile
         int buf = 0;
         bool ok = true;
-        for (int t = t0; t < t1 && ok; ++seg) {
+        for (int t = t0; t < t1 && ok; ++run) {
             const int r = t / p.ct, b = r / p.mt, m = r - b * p.mt;
             int j = t - r * p.ct;
-            const int je = min(p.ct, j + (t1 - t));
-            const bool whole = je - j == p.ct, head = t == t0;
+            // the block's tiles of this row tile are [j0, j1), this run's [j, je)
+            const int j0 = max(0, t0 - r * p.ct), j1 = min(p.ct, j + (t1 - t)), je = min(j1, j + RUN);
+            const bool whole = j1 - j0 == p.ct, head = r * p.ct <= t0, begun = j > j0, more = je < j1;
             t += je - j;
             const int grow = m * FR + row;
             float off = 0.f, w = 0.f;
@@ -462,7 +473,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(P_FULL(sb));
             }
-            if (!ok || !mbar_wait_warp(O_FULL, seg & 1, abortp)) break;
+            if (!ok || !mbar_wait_warp(O_FULL, run & 1, abortp)) break;
             tc_fence_after();
             const bool rin = grow < p.M;
             uint32_t v[DN / 64][32];
@@ -476,10 +487,23 @@ __global__ void __launch_bounds__(F_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < DN / 64; ++c) {
                 const int col = grp * (DN / 2) + c * 32;
-                if (!whole) {
+                // the block's place for its first row tile, or for the one it is at (a thread's own part:
+                // nobody else reads it before the kernel's end)
+                float4 *part = reinterpret_cast<float4 *>(
+                    p.parts + ((static_cast<int64_t>(blockIdx.x) * 2 + (head ? 0 : 1)) * FR + row) * DN + col);
+                if (begun) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 a = part[k];
+                        v[c][k * 4] = __float_as_uint(__uint_as_float(v[c][k * 4]) + a.x);
+                        v[c][k * 4 + 1] = __float_as_uint(__uint_as_float(v[c][k * 4 + 1]) + a.y);
+                        v[c][k * 4 + 2] = __float_as_uint(__uint_as_float(v[c][k * 4 + 2]) + a.z);
+                        v[c][k * 4 + 3] = __float_as_uint(__uint_as_float(v[c][k * 4 + 3]) + a.w);
+                    }
+                }
+                if (more || !whole) {
                     // (rows and values beyond the result too: nothing reads them)
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        p.parts + ((static_cast<int64_t>(blockIdx.x) * 2 + (head ? 0 : 1)) * FR + row) * DN + col);
+                    uint4 *dst = reinterpret_cast<uint4 *>(part);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[c][k * 4], v[c][k * 4 + 1], v[c][k * 4 + 2], v[c][k * 4 + 3]);
                     continue;

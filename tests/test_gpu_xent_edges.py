@@ -26,3 +26,65 @@ def test_rows_and_labels_that_part_a_warp(cuda_device, dtype, N, K, d):
         assert km.km_device_error() == 0
         _check_loss(X, C, ids, scale, loss, lse)
         _check_grad(X, C, ids, g, scale, dX, dC, parts=2 if K <= 128 and d <= 128 and dtype != torch.float32 else 1)
+
+
+def _fp64(X, C, ids, g, scale=1.0, block=8192):
+    """(loss, lse, dX, dC) of one batch in 64 bits on the device."""
+    C6, N = C.double(), X.shape[0]
+    loss, lse = torch.zeros(N, dtype=torch.float64, device=X.device), torch.zeros(N, dtype=torch.float64, device=X.device)
+    rX, rC = torch.zeros(X.shape, dtype=torch.float64, device=X.device), torch.zeros_like(C6)
+    for n in range(0, N, block):
+        s = slice(n, n + block)
+        x = X[s].double()
+        z = scale * (x @ C6.t())
+        lse[s] = torch.logsumexp(z, 1)
+        ok = (ids[s] >= 0) & (ids[s] < C.shape[0])
+        rows, t = ok.nonzero()[:, 0], ids[s][ok].long()
+        loss[n + rows] = lse[n + rows] - z[rows, t]
+        p = torch.exp(z - lse[s, None])
+        p[rows, t] -= 1
+        w = torch.zeros(x.shape[0], dtype=torch.float64, device=X.device)
+        w[rows] = g[s][rows].double() * scale
+        p[~ok] = 0
+        p *= w[:, None]
+        rX[s] = p @ C6
+        rC += p.t() @ torch.where(ok[:, None], x, torch.zeros_like(x))
+    return loss, lse, rX, rC
+
+
+def _drift(got, ref):
+    """The common relative error of the entries: the slope of got over ref, less one."""
+    return (((got.double() - ref) * ref).sum() / (ref * ref).sum()).item()
+
+
+def _one_signed(N, K, d, dtype, dev, g):
+    # positive points against positive rows; labels among the first ten rows, which are zero, so that
+    # every gradient beyond them is a sum of terms of one sign
+    gen = torch.Generator(device=dev).manual_seed(1)
+    X = torch.randn((N, d), generator=gen, device=dev).abs().to(dtype)
+    C = (torch.randn((K, d), generator=gen, device=dev).abs() * (0.2 / d ** 0.5)).to(dtype)
+    C[:10] = 0
+    ids = torch.randint(0, 10, (N,), generator=gen, device=dev, dtype=torch.int32)
+    return X, C, ids, torch.full((N,), g, device=dev)
+
+
+# An addition of the tensor cores is off by at most 2^-23 of the running sum; 1024 of them, the most that
+# one accumulator takes, by 1024 2^-23 of a sum of one sign. The rest (exponentials, lse: 2^-18 at these
+# logits; roundings of P and of the result, which have no common direction) stays below 2^-16.
+MAX_DRIFT = 1024 * 2.0 ** -23 + 2.0 ** -16
+
+
+@pytest.mark.parametrize("N,K,d,g", [
+    (1 << 18, 1 << 14, 128, 1.0),       # dC: 1771 tiles of points to a block
+    (1 << 22, 100, 64, 0.25),           # few table rows, P in two parts: 221 tiles of 16 products
+    (1 << 14, 1 << 17, 128, 1.0),       # dX: 885 tiles of table rows to a block
+])
+def test_long_reductions_of_short_rows_do_not_drift(cuda_device, N, K, d, g):
+    X, C, ids, gr = _one_signed(N, K, d, torch.float16, cuda_device, g)
+    loss, lse = km.km_xent(X[None], C[None], ids[None])
+    dX, dC = km.km_xent_grad(X[None], C[None], ids[None], lse, gr[None])
+    torch.cuda.synchronize()
+    assert km.km_device_error() == 0
+    _, _, rX, rC = _fp64(X, C, ids, gr, block=(1 << 27) // K)
+    assert abs(_drift(dC[0, 10:], rC[10:])) <= MAX_DRIFT
+    assert abs(_drift(dX[0], rX)) <= MAX_DRIFT
