@@ -34,7 +34,9 @@ inline int64_t piece_rows(int64_t B, int64_t N, int64_t K) {
 // waves * (64-wide steps of a split + 4 to start and drain) at 0.3 us a step, plus the writing and
 // reading of the splits' fp32 partials at 4 TB/s and a launch. (dC of a 4096-row table over 32768 points
 // at d = 256, 16 tiles: 253 us unsplit, 161 in the chosen four; dX, 128 tiles: 152 unsplit as chosen, 189 in
-// two.) The CUDA cores work on 128 x 128 tiles and split where those leave SMs idle, each split at least
+// two.) No split is longer than 256 steps, kMaxChain products: its additions truncate, and the splits are joined
+// in fp32 (65536 points, 2048 rows, d = 1024: one-signed sums 2.1e-4 too small in splits of 512 steps, 1.0e-4
+// in these). The CUDA cores work on 128 x 128 tiles and split where those leave SMs idle, each split at least
 // 512 long.
 inline int64_t product_splits(int64_t B, int64_t M, int64_t N, int64_t Kk, km_dtype dt) {
     const int64_t steps = ceil_div(Kk, TKC);
@@ -45,14 +47,15 @@ inline int64_t product_splits(int64_t B, int64_t M, int64_t N, int64_t Kk, km_dt
         return ceil_div(steps, ceil_div(steps, want));
     }
     const int64_t tiles = B * ceil_div(M, 2 * TBM) * ceil_div(N, TBN);
-    int64_t best = 1;
+    const int64_t least = ceil_div(steps, kMaxChain / 4);
+    int64_t best = least;
     double best_us = 0;
-    for (int64_t s = 1; s <= 64 && s <= steps; ++s) {
+    for (int64_t s = least; s <= std::max<int64_t>(64, least) && s <= steps; ++s) {
         const int64_t per = ceil_div(steps, s), splits = ceil_div(steps, per);
         if (splits != s) continue;      // the same pieces as with fewer splits
         const double us = 0.3 * static_cast<double>(ceil_div(tiles * s, 74)) * static_cast<double>(per + 4) +
                           (s > 1 ? 3.0 + 8e-6 / 4 * static_cast<double>(s * B * M * N) : 0.0);
-        if (s == 1 || us < best_us) {
+        if (s == least || us < best_us) {
             best = s;
             best_us = us;
         }

@@ -88,3 +88,18 @@ def test_long_reductions_of_short_rows_do_not_drift(cuda_device, N, K, d, g):
     _, _, rX, rC = _fp64(X, C, ids, gr, block=(1 << 27) // K)
     assert abs(_drift(dC[0, 10:], rC[10:])) <= MAX_DRIFT
     assert abs(_drift(dX[0], rX)) <= MAX_DRIFT
+
+
+@pytest.mark.parametrize("N,K,d,g", [
+    (65536, 2048, 1024, 0.25),          # dC: 1024 steps of 64 points
+    (1024, 1 << 17, 512, 1.0),          # dX: 2048 steps of 64 table rows
+])
+def test_long_reductions_of_long_rows_do_not_drift(cuda_device, N, K, d, g):
+    X, C, ids, gr = _one_signed(N, K, d, torch.float16, cuda_device, g)
+    loss, lse = km.km_xent(X[None], C[None], ids[None])
+    dX, dC = km.km_xent_grad(X[None], C[None], ids[None], lse, gr[None])
+    torch.cuda.synchronize()
+    assert km.km_device_error() == 0
+    _, _, rX, rC = _fp64(X, C, ids, gr, block=(1 << 27) // K)
+    assert abs(_drift(dC[0, 10:], rC[10:])) <= MAX_DRIFT
+    assert abs(_drift(dX[0], rX)) <= MAX_DRIFT
