@@ -14,6 +14,10 @@ namespace km {
 namespace mv4 {
 
 constexpr int kKmax = 16;
+// Additions of the tensor cores truncate, up to 1.3e-7 of the sum each where all terms have one sign (measured:
+// rows of 2^22 codes, 32768 products to a warp, 3.3e-3 too small). After this many the sum goes on in fp32: 1.3e-4,
+// less than half of fp16's half step.
+constexpr int kMaxChain = 1024;
 
 // codes [R,N] -> packed [R, pitch]; one thread per 16 bytes (32 codes), padding codes 0. VEC: rows are
 // whole 16-byte units (32768 x 8192: 58 us, 6.9 TB/s; byte by byte 246).
@@ -233,12 +237,16 @@ __device__ __forceinline__ bool mbar_ready(uint32_t bar, uint32_t parity, volati
 namespace km {
 namespace mv4 {
 
-// SC: 0 no scales, 1 groups of whole 128-code blocks, 2 any multiple of 32.
+// SC: 0 no scales, 1 groups of whole 128-code blocks, 2 any multiple of 32, 3 no scales and rows so long that a
+// warp's sum must end after kMaxChain products (a form of its own: the second sum's registers cost 32 tokens
+// x 4096 x 4096 13.0 to 14.4 us).
 template <typename T, bool XV, int NT, int SC>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     matvec4_mma_kernel(const __grid_constant__ CUtensorMap tm, const T *__restrict__ x, const MmaParams p,
                        T *__restrict__ y) {
     constexpr int XD = NT > 2 ? 2 : 4;       // chunks of tokens held ahead
+    constexpr bool scaled = SC == 1 || SC == 2;
+    constexpr int kRun = kMaxChain / 8;      // (SC 3) stages, of eight products a warp, to a sum
     constexpr int kCodesPerStage = 2 * kStageRow;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[2][2 * kMmaStages];
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             xr[n] = x + min(m0 + n * 8 + g, p.M - 1) * p.N + warp * 128 + t * 8;
         }
         const float *sa = nullptr, *sb = nullptr;
-        if (SC) {
+        if (scaled) {
             sa = p.scales + min(r0 + g, p.R - 1) * p.ngroups;
             sb = p.scales + min(r0 + g + 8, p.R - 1) * p.ngroups;
         }
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         if (nfull > 0) {
 #pragma unroll
             for (int h = 0; h < XD; ++h) next_x(h, 0, h);
-            if (SC) read_scales(0, nxa, nxb);
+            if (scaled) read_scales(0, nxa, nxb);
         }
         {
             // pair tables: this thread's row, the 16 entries with high code `hi`; every thread holds
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             values[half][ht >> 4][ht & 15] = bits16(Cvt<T>::from_f(cval));
             named_barrier_sync(1 + half, kHalfThreads);       // and the previous tile's sums are read
             cval = codebook_value(item + step);
-            if (SC) {
+            if (scaled) {
                 // the next tile's scales into L2
                 const int64_t r1 = static_cast<int64_t>((item + step) % p.rtiles) * 16 + (ht >> 4);
                 if (item + step < p.items && r1 < p.R)
@@ -453,6 +461,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 else next_x(h + XD - 4, ahead, h % XD);
                 if (SC == 2) add(__shfl_sync(0xffffffffu, sca, (lane & 28) + h), __shfl_sync(0xffffffffu, scb, (lane & 28) + h));
             }
+            if (SC == 3 && s % kRun == kRun - 1) add(1.f, 1.f);
             if (SC == 1) add(__shfl_sync(0xffffffffu, sca, (lane & 28) + (s & 3)), __shfl_sync(0xffffffffu, scb, (lane & 28) + (s & 3)));
 #pragma unroll
             for (int n = 0; n < NT; ++n) xr[n] += kCodesPerStage;
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma16816<T>(SC ? acc[n] : tot[n], f, xt[n][2 * j], xt[n][2 * j + 1]);
                 }
-                if (SC) {
+                if (scaled) {
                     const uint32_t gi = fd_div(p.cpg, q0 + h);
                     add(sa[gi], sb[gi]);
                 }
@@ -492,6 +501,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             if (lane == 0) mbar_arrive(empty0 + 8 * slot);
             if (++slot == kMmaStages) { slot = 0; ph ^= 1u; }
         }
+        if (SC == 3) add(1.f, 1.f);
         // the warps' sums, joined in warp order, through the table's place: [warp][token][17]
         if (named_barrier_or(1 + half, kHalfThreads, !ok)) break;
         float *red = reinterpret_cast<float *>(smem + (tab - base));
@@ -578,7 +588,8 @@ km_status mma_tokens(const CUtensorMap &tm, const T *x, const MmaParams &p, T *y
 }
 template <typename T, bool XV>
 km_status mma_scales(const CUtensorMap &tm, const T *x, const MmaParams &p, T *y, cudaStream_t st) {
-    if (!p.scales) return mma_tokens<T, XV, 0>(tm, x, p, y, st);
+    // a warp takes an eighth of the row, 16 codes to a product
+    if (!p.scales) return p.N <= 8 * 16 * kMaxChain ? mma_tokens<T, XV, 0>(tm, x, p, y, st) : mma_tokens<T, XV, 3>(tm, x, p, y, st);
     return p.cpg.d % 4 == 0 ? mma_tokens<T, XV, 1>(tm, x, p, y, st) : mma_tokens<T, XV, 2>(tm, x, p, y, st);
 }
 // tcgen05 form: rows of x in whole 16-byte units.

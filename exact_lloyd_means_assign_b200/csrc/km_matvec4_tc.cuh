@@ -51,6 +51,8 @@ template <int NTOK, int SC> struct TcMv {
     static constexpr uint32_t kXBytes = kStep / 64 * kXChunk;
     static constexpr uint32_t kStage = kCodeBytes + kXBytes;
     static constexpr int kSub = SC ? kStep / (256 >> SC) : 1;      // accumulators per step
+    // Without scales a sum ends after kMaxChain products all the same: their additions truncate.
+    static constexpr int kRun = SC ? 1 : kMaxChain / (kStep / 16);  // steps to a set of accumulators
     static constexpr uint32_t kAcc = kSub * NTOK;                 // their TMEM columns
     static constexpr int kDBufs = 2 * kAcc + kStep > 512 ? 1 : 2;  // sets of accumulators
     static constexpr uint32_t kACol = kDBufs * kAcc;               // decoded steps behind them
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (item + stride < items && r1 < p.R)
                     for (int o = 0; o < p.ngroups; o += 32) prefetch_l2(p.scales + r1 * p.ngroups + o);
             }
-            const int reads = SC ? nst : (nst ? 1 : 0);
+            const int reads = (nst + L::kRun - 1) / L::kRun;
 #pragma unroll 1
             for (int s = 0; s < reads; ++s) {
                 float sc[L::kSub];
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int i = 0; i < NTOK; ++i)
                             tot[i] = SC ? fmaf(sc[u + k], __uint_as_float(v[k * NTOK + i]), tot[i])
-                                        : __uint_as_float(v[i]);
+                                        : tot[i] + __uint_as_float(v[i]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int item = first; item < items && ok; item += stride) {
 #pragma unroll 1
             for (int s = 0; s < nst; ++s) {
-                const bool new_acc = SC || s == 0, end_acc = SC || s + 1 == nst;
+                const bool new_acc = s % L::kRun == 0, end_acc = (s + 1) % L::kRun == 0 || s + 1 == nst;
                 if (new_acc && !mbar_ready(D_EMPTY(db), dph, abortp)) { ok = false; break; }
                 if (!mbar_ready(FULL(slot), ph, abortp) || !mbar_ready(A_FULL(ab), aph, abortp)) {
                     ok = false;
