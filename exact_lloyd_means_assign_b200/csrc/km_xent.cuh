@@ -55,6 +55,10 @@ __device__ __forceinline__ float p_factor(const unsigned int *wmax, float s, boo
     return inverse ? m / s : s / m;
 }
 
+// What a sum of exponentials is taken against, given the maximum of its logits: the maximum, or 0 where that
+// is infinite (every logit masked: the sum is then 0 instead of NaN).
+__device__ __forceinline__ float sum_base(float m) { return isinf(m) ? 0.f : m; }
+
 // Two fp32 values in one register pair, for the packed fp32 arithmetic of sm_100.
 __device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
     uint64_t r;
@@ -208,10 +212,11 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             float s = 0.f;
+            const float base = sum_base(m);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int col = n0 + (j & 3) + tx * 4 + (j >> 2) * 64;
-                if (col < N) s += expf(acc[i][j] - m);
+                if (col < N) s += expf(acc[i][j] - base);
             }
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -277,14 +282,14 @@ __global__ void __launch_bounds__(256)
 #pragma unroll 8
         for (int t = q; t < tiles; t += 8) {
             const float2 v = pr[static_cast<int64_t>(t) * N];
-            s = fmaf(v.y, expf(v.x - m), s);
+            s = fmaf(v.y, v.x == m ? 1.f : expf(v.x - m), s);      // (equal infinities)
         }
     part[q][x] = s;
     __syncthreads();
     if (q == 0 && in) {
 #pragma unroll
         for (int i = 1; i < 8; ++i) s += part[i][x];
-        const float l = m + logf(s);
+        const float l = s == 0.f ? m : m + logf(s);     // (0: all logits at the ends of fp32, or masked)
         const int64_t at = b * N + row;
         const int id = ids[at];
         if (lse) lse[at] = l;

@@ -259,6 +259,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
         // The products are formed with |scale| (a negative scale negates the points in the MMA).
         const float sc = fabsf(ep.scale), s2 = sc * kLog2e;
         const uint64_t s22 = pair_f32(s2, s2);
+        // kLse: a maximum below this (every logit so far masked by an infinity or by the type's lowest value) would
+        // overflow as the sums' base; their terms are 0 then.
+        const float floor_ = -3e38f / fmaxf(s2, 1.f);
         const float fac = MODE == kProb ? p_factor(ep.wmax, ep.pscale, false) : 1.f;
         const float inv = MODE == kOut && ep.splits == 1 ? p_factor(ep.wmax, ep.pscale, true) : 1.f;
         const uint32_t obuf = sbase + Sh::kOutOff + (warp - T_EPI0) * 2 * kOutBuf;
@@ -345,21 +348,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                         }
                         cm = max3f(max3f(cm, __uint_as_float(v[CH - 2]), __uint_as_float(v[CH - 1])), cm2, cm);
                         const float nm = ch ? fmaxf(m, cm) : cm;
-                        if (ch) {
-                            const float corr = ex2f((m - nm) * s2);
-                            const uint64_t c2 = pair_f32(corr, corr);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) s4[i] = fma2(s4[i], c2, 0ull);
-                        }
-                        m = nm;
-                        const float d = -nm * s2;
-                        const uint64_t d2 = pair_f32(d, d);
-#pragma unroll
-                        for (int i = 0; i < CH; i += 2) {
-                            float a, b;
-                            unpair_f32(fma2(pair_f32(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s22, d2), a, b);
-                            s4[(i >> 1) & 3] = add2(s4[(i >> 1) & 3], pair_f32(ex2f(a), ex2f(b)));
-                        }
                         if (label >= col && label < col + CH) {
                             asm volatile("");
                             float zt = 0.f;
@@ -367,6 +355,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                             for (int i = 0; i < CH; ++i)
                                 if (col + i == label) zt = __uint_as_float(v[i]) * sc;
                             ep.zt[br] = zt;
+                        }
+                        if (ch) {
+                            const float corr = ex2f((fmaxf(m, floor_) - fmaxf(nm, floor_)) * s2);
+                            const uint64_t c2 = pair_f32(corr, corr);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s4[i] = fma2(s4[i], c2, 0ull);
+                        }
+                        m = nm;
+                        // the product rounded down where its rounding could pass for a large exponent
+                        const float top = fmaxf(nm, floor_), d = fabsf(top) * s2 > 0x1p20f ? __fmul_rd(-top, s2) : -top * s2;
+                        const uint64_t d2 = pair_f32(d, d);
+#pragma unroll
+                        for (int i = 0; i < CH; i += 2) {
+                            float a, b;
+                            unpair_f32(fma2(pair_f32(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s22, d2), a, b);
+                            s4[(i >> 1) & 3] = add2(s4[(i >> 1) & 3], pair_f32(ex2f(a), ex2f(b)));
                         }
                     }
                 } else if (MODE == kProb) {

@@ -435,6 +435,9 @@ km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int
  *     z[n,k] = scale * <X[b,n], C[b,k]>,  lse[b,n] = log sum_k exp(z[n,k]),
  *     loss[b,n] = lse[b,n] - z[n, ids[b,n]], 0 where ids[b,n] is outside [0,K) (no label).
  * X[B,N,d], C[B,K,d] in `dtype`; loss[B,N], lse[B,N] fp32 out, either may be NULL.
+ * A table row may be masked by a coordinate that brings its logits to minus infinity or far below the
+ * others, the type's lowest value included: it adds nothing to lse. With every logit minus infinity lse is
+ * minus infinity; a logit of plus infinity gives NaN.
  *
  * km_xent_grad: with P[n,k] = g[n] * scale * (exp(z[n,k] - lse[n]) - [k = id_n]), 0 for points
  * without a label,
@@ -446,7 +449,9 @@ km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int
  * (fp16: times 2^14, so that small probabilities keep their bits; in two parts for tables of up to 128
  * rows of up to 128 values); all sums are fp32, in an order fixed
  * by the sizes and the number of SMs. Points without a label may hold any values: they reach neither
- * gradient (their own rows of dX are zero).
+ * gradient (their own rows of dX are zero). An infinite value of the table makes dX NaN in its column, as
+ * the formula has it (0 times infinity); dC stays as if the masked row were absent. To train with masked
+ * rows, mask them with a finite value.
  *
  * ws: km_xent_workspace_size / km_xent_grad_workspace_size bytes, 256-byte aligned (0 for sizes
  * that are not provided; asked for with the device of the call current). Calls that may overlap need

@@ -103,3 +103,55 @@ def test_long_reductions_of_long_rows_do_not_drift(cuda_device, N, K, d, g):
     _, _, rX, rC = _fp64(X, C, ids, gr, block=(1 << 27) // K)
     assert abs(_drift(dC[0, 10:], rC[10:])) <= MAX_DRIFT
     assert abs(_drift(dX[0], rX)) <= MAX_DRIFT
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("low", ["inf", "lowest", "large"])
+@pytest.mark.parametrize("d", [40, 64, 136])
+@pytest.mark.parametrize("K,dead", [(700, [(0, 200), (500, 700)]), (90, [(0, 64), (80, 90)]), (1500, [(100, 1400)]),
+                                    (300, [(0, 1), (64, 128), (256, 300)]), (600, [(0, 256)])])
+def test_masked_table_rows(cuda_device, dtype, low, d, K, dead):
+    # a column of ones against a column of the table that holds minus infinity, the type's lowest value or
+    # another large one where a row is masked: whole chunks and tiles of logits are, and the result is that of the table
+    # without those rows
+    N = 150
+    X, C, _, g = _inputs(1, N, K, d, dtype, cuda_device, seed=K + d)
+    g = g.abs() + 1.0 / N
+    X[..., -1] = 1
+    C[..., -1] = 0
+    alive = torch.ones(K, dtype=torch.bool, device=cuda_device)
+    for a, b in dead:
+        alive[a:b] = False
+    sub = C[:, alive].contiguous()
+    to_sub = torch.cumsum(alive, 0) - 1
+    rows = alive.nonzero()[:, 0]
+    ids = rows[torch.arange(N, device=cuda_device) * 7 % len(rows)].to(torch.int32)[None].contiguous()
+    ids[0, ::9] = -1
+    ids_sub = torch.where(ids >= 0, to_sub[ids.clamp(min=0).long()].to(torch.int32), ids)
+    for scale in (1.0, -0.5):
+        value = {"inf": -float("inf"), "lowest": torch.finfo(dtype).min, "large": -3e4 if dtype == torch.float16 else -1e30}[low]
+        C[:, ~alive, -1] = value if scale > 0 else -value
+        loss, lse = km.km_xent(X, C, ids, scale)
+        dX, dC = km.km_xent_grad(X, C, ids, lse, g, scale)
+        torch.cuda.synchronize()
+        assert km.km_device_error() == 0
+        _check_loss(X, sub, ids_sub, scale, loss, lse)
+        # (with infinities the formula's dX is NaN: 0 times infinity)
+        _check_grad(X, sub, ids_sub, g, scale, dX if low != "inf" else None, dC[:, alive].contiguous())
+        assert (dC[:, ~alive] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 136])
+def test_every_row_masked(cuda_device, dtype, d):
+    X, C, ids, _ = _inputs(1, 70, 400, d, dtype, cuda_device, seed=d)
+    X[..., -1] = 1
+    C[..., -1] = -float("inf")
+    loss, lse = km.km_xent(X, C, torch.full_like(ids, -1))
+    assert (lse == -float("inf")).all() and (loss == 0).all()
+    for low in (torch.finfo(dtype).min, torch.finfo(dtype).min / 2, -3e4):
+        C[..., -1] = low
+        loss, lse = km.km_xent(X, C, ids)
+        # (at 32-bit ranges log K is below the resolution of lse)
+        assert torch.isfinite(loss).all()
+        assert ((lse.double() - low).abs() <= 2.0 ** -8 * abs(low) + 20).all()
