@@ -103,6 +103,7 @@ struct FusedWs {
     float *w, *parts;
     unsigned int *wmax;
     PointTile *points;
+    PointRow *rows;
     int64_t ptiles;
 };
 inline FusedWs carve_fused(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d, km_dtype dt) {
@@ -114,6 +115,7 @@ inline FusedWs carve_fused(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d
     f.w = c.take<float>(static_cast<size_t>(B * N) * 4);
     f.wmax = c.take<unsigned int>(4);
     f.points = c.take<PointTile>(static_cast<size_t>(B * f.ptiles) * sizeof(PointTile));
+    f.rows = c.take<PointRow>(static_cast<size_t>(B * f.ptiles) * FR * sizeof(PointRow));
     f.parts = c.take<float>(static_cast<size_t>(fused_blocks(fused_tiles(B, N, K))) * 2 * FR * (d > 64 ? 128 : 64) * 4);
     return f;
 }
@@ -344,6 +346,7 @@ km_status fused_launch(const void *A, const void *Bo, int64_t B, int64_t M, int6
     p.idesc_s = km::mma_idesc_f16(bf16 ? 1u : 0u, FR, FR) | (scale < 0.f ? 1u << 13 : 0u);   // bit 13 negates A
     p.idesc_o = km::mma_idesc_f16(bf16 ? 1u : 0u, FR, DN) | (1u << 16);                      // B MN-major
     p.points = w.points;
+    p.rows = w.rows;
     p.wmax = w.wmax;
     p.pscale = pscale;
     p.parts = w.parts;
@@ -359,7 +362,8 @@ km_status fused_launch(const void *A, const void *Bo, int64_t B, int64_t M, int6
     auto join = [&](auto parts, int units) {
         constexpr int PARTS = decltype(parts)::value;
         fused_join_kernel<T, DN, PARTS><<<static_cast<unsigned>(units) * (FR * PARTS / 4), DN, 0, st>>>(
-            w.parts, p.tiles, blocks, p.M, p.d, p.mt, p.ct, w.wmax, pscale, static_cast<T *>(out));
+            w.parts, p.tiles, blocks, p.M, p.d, p.mt, p.ct, COL ? nullptr : w.rows, w.wmax, pscale,
+            static_cast<T *>(out));
     };
     // (from 16 blocks to a row tile on, its partials are worth sharing out)
     if (blocks >= 16 * rows) join(std::integral_constant<int, 4>(), rows);
@@ -395,7 +399,7 @@ km_status fused_grads(const void *X, km_dtype dt, const void *C, const int32_t *
         g, ids, B * N, static_cast<int>(K), scale, w.w, w.wmax);
     if (launch_status() != KM_OK) return KM_ERR_CUDA;
     point_param_kernel<<<fill_blocks(B * w.ptiles * FR), 256, 0, st>>>(w.w, lse, ids, B, static_cast<int>(N), w.ptiles,
-                                                                static_cast<int>(K), w.wmax, pscale, w.points);
+                                                                static_cast<int>(K), w.wmax, pscale, w.points, w.rows);
     if (launch_status() != KM_OK) return KM_ERR_CUDA;
     // points without a label become zeros, so that nothing they hold reaches a sum
     if ((s = copy_rows<T>(X, ids, B * N, d, dp, K, w.X, st)) != KM_OK) return s;

@@ -49,6 +49,7 @@ struct Epi {
 // itself (half a step of the type), which no sum over tokens averages away; relative to the maximum it
 // is near -1, which has none of that. s is 1, and 2^14 for fp16, whose normal range ends at 2^-14:
 // probabilities down to 2^-28 keep their bits. The products are multiplied by max |w| / s in fp32.
+// (The rows of P of dX alone, in km_xent_fused.cuh, are each relative to their own weight.)
 __device__ __forceinline__ float p_factor(const unsigned int *wmax, float s, bool inverse) {
     if (!wmax) return 1.f;
     const float m = fminf(fmaxf(__uint_as_float(*wmax), 0x1p-100f), 0x1p100f);

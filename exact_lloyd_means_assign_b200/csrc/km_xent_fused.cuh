@@ -44,6 +44,14 @@ struct __align__(16) PointTile {
     int label[FR];
 };
 
+// The same of one point where it is a row of P (dX): relative to its own weight, so that what a row of dX
+// holds does not depend on the other points' weights; `factor`, |w| / s, is put back in the result. off = log2 s -
+// lse log2 e, w = s with the weight's sign.
+struct __align__(16) PointRow {
+    float off, w, factor;
+    int label;
+};
+
 template <int DN, bool COL> struct FShape {
     static constexpr int kChunks = DN / 64;
     static constexpr uint32_t kTile = FR * DN * 2;
@@ -79,7 +87,8 @@ struct FParams {
     int tiles;                // mt * ct * batches, shared out over the blocks
     float scale;              // |scale|
     uint32_t idesc_s, idesc_o;
-    const PointTile *points;  // [batches][tiles of points]
+    const PointTile *points;  // [batches][tiles of points] (dC)
+    const PointRow *rows;     // [batches][tiles of points][128] (dX)
     const unsigned int *wmax;
     float pscale;
     float *parts;             // [blocks][2][128][DN]: a block's first and last row tile, where shared
@@ -97,7 +106,7 @@ __host__ __device__ inline int fused_begin(int tiles, int blocks, int block) {
 __global__ void __launch_bounds__(256)
     point_param_kernel(const float *__restrict__ w, const float *__restrict__ lse, const int32_t *__restrict__ ids,
                        int64_t B, int N, int64_t tiles, int K, const unsigned int *__restrict__ wmax, float pscale,
-                       PointTile *__restrict__ out) {
+                       PointTile *__restrict__ out, PointRow *__restrict__ rows) {
     const float fac = p_factor(wmax, pscale, false);
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < B * tiles * FR; i += gridDim.x * 256ll) {
         const int64_t t = i / FR, b = t / tiles;
@@ -105,17 +114,26 @@ __global__ void __launch_bounds__(256)
         const int64_t n = (t - b * tiles) * FR + k;
         float off = -INFINITY, v = 0.f;
         int label = -1;
+        PointRow row = {-INFINITY, 0.f, 0.f, -1};
         if (n < N) {
             const int id = ids[b * N + n];
             if (id >= 0 && id < K) {
-                v = w[b * N + n] * fac;
-                off = __log2f(fabsf(v)) - lse[b * N + n] * kLog2e;
+                const float wn = w[b * N + n], l = lse[b * N + n] * kLog2e;
+                v = wn * fac;
+                off = __log2f(fabsf(v)) - l;
                 label = id;
+                row.label = id;
+                if (wn != 0.f) {
+                    row.off = __log2f(pscale) - l;
+                    row.w = wn < 0.f ? -pscale : pscale;
+                    row.factor = fabsf(wn) / pscale;
+                }
             }
         }
         out[t].off[k] = off;
         out[t].w[k] = v;
         out[t].label[k] = label;
+        rows[i] = row;
     }
 }
 
@@ -338,7 +356,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const float s2 = p.scale * kLog2e;
         const uint64_t s22 = pair_f32(s2, s2);
-        const float inv = p_factor(p.wmax, p.pscale, true);
+        float inv = COL ? p_factor(p.wmax, p.pscale, true) : 0.f;
         int slot = 0, run = 0;
         uint32_t ph = 0, sph = 0, odd = 0;          // phases; parity of the tile
         int buf = 0;
@@ -354,10 +372,11 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             float off = 0.f, w = 0.f;
             int label = -1;
             if (!COL) {
-                const PointTile &pt = p.points[r];
-                off = pt.off[row];
-                w = pt.w[row];
-                label = pt.label[row];
+                const PointRow pt = p.rows[static_cast<int64_t>(r) * FR + row];
+                off = pt.off;
+                w = pt.w;
+                label = pt.label;
+                inv = pt.factor;
             }
             const uint32_t sgn = w < 0.f ? 0x80008000u : 0u;
             const uint64_t off2 = pair_f32(off, off);
@@ -559,11 +578,12 @@ __host__ __device__ inline int fused_owner(int tiles, int blocks, int tile) {
 // The row tiles that blocks share: their partials in block order. PARTS == 1: few partials to a row tile;
 // each product block c > 0 stands for the row tile in which it begins, and the first that begins inside it
 // (not at its start) answers. PARTS > 1: few row tiles, with up to all blocks' partials each, which PARTS
-// threads take in runs.
+// threads take in runs. rows: the factors of dX's rows, null for dC.
 template <typename T, int DN, int PARTS>
 __global__ void __launch_bounds__(DN)
     fused_join_kernel(const float *__restrict__ parts, int tiles, int blocks, int M, int d, int mt, int ct,
-                      const unsigned int *__restrict__ wmax, float pscale, T *__restrict__ out) {
+                      const PointRow *__restrict__ rows, const unsigned int *__restrict__ wmax, float pscale,
+                      T *__restrict__ out) {
     constexpr int ROWS = 4 / PARTS;      // rows of a row tile that a block takes
     __shared__ float4 sums[PARTS][DN / 4];
     const int unit = blockIdx.x / (FR / ROWS), part = PARTS == 1 ? 0 : threadIdx.x / (DN / 4);
@@ -604,7 +624,7 @@ __global__ void __launch_bounds__(DN)
 #pragma unroll
         for (int i = 1; i < PARTS; ++i) add(sums[i][col / 4]);
     }
-    const float inv = p_factor(wmax, pscale, true);
+    const float inv = rows ? rows[static_cast<int64_t>(r) * FR + row].factor : p_factor(wmax, pscale, true);
     const float f[4] = {s.x * inv, s.y * inv, s.z * inv, s.w * inv};
 #pragma unroll
     for (int k = 0; k < 4; ++k)

@@ -155,3 +155,28 @@ def test_every_row_masked(cuda_device, dtype, d):
         # (at 32-bit ranges log K is below the resolution of lse)
         assert torch.isfinite(loss).all()
         assert ((lse.double() - low).abs() <= 2.0 ** -8 * abs(low) + 20).all()
+
+
+@pytest.mark.parametrize("d,N,K", [(64, 300, 700), (128, 500, 90), (100, 20000, 300)])
+@pytest.mark.parametrize("low", [-12, -22, -26])
+def test_rows_of_small_weight_beside_large_ones(cuda_device, d, N, K, low):
+    # every second point weighs 2^low of the others; its row of dX is what it is alone: two roundings to half a
+    # step of the type (P, where sums over the table average it, and the result), and half a step of fp16's subnormals
+    dtype = torch.float16
+    X, C, ids, _ = _inputs(1, N, K, d, dtype, cuda_device, seed=d)
+    g = torch.full((1, N), 2.0 ** 13, device=cuda_device)
+    g[0, 1::2] = 2.0 ** (13 + low)
+    _, lse = km.km_xent(X, C, ids)
+    dX, dC = km.km_xent_grad(X, C, ids, lse, g)
+    _, _, rX, rC = _fp64(X[0], C[0], ids[0], g[0])
+    small, ref = dX[0, 1::2].double(), rX[1::2]
+    rounding = torch.clamp(ref.abs() * 2.0 ** -11, min=2.0 ** -25)
+    # (a row's entries of P are off by half a step each, 2^-11 of a probability, with independent signs: in the
+    # norm over a row's d values at most 2^-11 |p - label| |C|, the label's entry having no such error)
+    assert (small - ref).norm() <= rounding.norm() + 2.0 ** -11 * ref.norm()
+    assert ((small - ref).abs() <= 2 * rounding + 2.0 ** -11 * ref.norm(dim=1, keepdim=True) * 4 / d ** 0.5).all()
+    # and equal bits whatever the others weigh
+    g2 = g.clone()
+    g2[0, ::2] = 2.0 ** (13 + low)
+    alone, _ = km.km_xent_grad(X, C, ids, lse, g2)
+    assert torch.equal(alone[0, 1::2], dX[0, 1::2])
