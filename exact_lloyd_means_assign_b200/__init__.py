@@ -407,12 +407,16 @@ def km_init_kmeanspp1d(X, K, u, w=None, want_chosen=False, stream=None):
 
 
 def _dims(t, name, n):
+    if t is None:
+        raise ValueError(f"{name} is required")
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got {tuple(t.shape)}")
 
 
 def _on_gpu(t, name):
     """The CUDA device that an operator's first argument lies on; all others must share it."""
+    if t is None:
+        raise ValueError(f"{name} is required")
     dev = t.device
     if dev.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -504,9 +508,10 @@ def km_matvec4(x, packed, C, scales=None, group=0, y=None, stream=None):
     dev = _on_gpu(x, "x")
     _dims(x, "x", 2)
     N = x.shape[1]
-    if C.dim() == 3 and C.shape[2] == 1:
+    if C is not None and C.dim() == 3 and C.shape[2] == 1:
         C = C.view(C.shape[0], C.shape[1])
     _dims(C, "C", 2)
+    _dims(packed, "packed", 2)
     R = C.shape[0]
     _need(C, "C", torch.float32, None, dev)
     _need(packed, "packed", torch.uint8, (R, 16 * (-(-N // 32))), dev)
@@ -559,6 +564,7 @@ def km_lookup_grad(dY, ids, K, scale=1.0, dC=None, out_dtype=None, accumulate=Fa
     added to the given dC."""
     dev = _on_gpu(dY, "dY")
     _dims(dY, "dY", 3)
+    _dims(ids, "ids", 2)
     _need(ids, "ids", torch.int32, dY.shape[:2], dev)
     if accumulate and dC is None:
         raise ValueError("accumulate needs dC")
@@ -585,6 +591,7 @@ def _xent_args(X, C, ids):
     dev = _on_gpu(X, "X")
     _dims(X, "X", 3)
     _dims(C, "C", 3)
+    _dims(ids, "ids", 2)
     B, N, d = X.shape
     _need(C, "C", X.dtype, (B, C.shape[1], d), dev)
     _need(ids, "ids", torch.int32, (B, N), dev)
@@ -622,6 +629,7 @@ def km_xent_grad(X, C, ids, lse, g=None, scale=1.0, dX=None, dC=None, want_dX=Tr
     """Gradients of sum_n g[b,n] * loss[b,n] of km_xent (lse as it returned it; g [B,N] fp32, None =
     ones). Returns (dX [B,N,d], dC [B,K,d]) in X's dtype, None where not wanted."""
     dev = _xent_args(X, C, ids)
+    _dims(lse, "lse", 2)
     _need(lse, "lse", torch.float32, X.shape[:2], dev)
     _need(g, "g", torch.float32, X.shape[:2], dev)
     return _launch(dev, stream, _xent_grad, X, C, ids, lse, g, scale, dX, dC, want_dX, want_dC, ws)
