@@ -296,7 +296,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (SC) {
 #pragma unroll
                     for (int u = 0; u < L::kSub; ++u) {
-                        const int g = static_cast<int>(fd_div(p.cpg, min((st0 + s) * (STEP / 32) + u * (STEP / 32 / L::kSub), chunks - 1)));
+                        // (behind the row's end lie sums of zeros: no group, since the last may be infinite)
+                        const int chunk = (st0 + s) * (STEP / 32) + u * (STEP / 32 / L::kSub);
+                        const int g = chunk < chunks ? static_cast<int>(fd_div(p.cpg, chunk)) : p.ngroups;
                         if ((g >> 2) != unit) {      // groups come in order, one unit after the other
                             unit = g >> 2;
                             cur = nxt;

@@ -32,3 +32,22 @@ def test_long_rows_do_not_drift(cuda_device, dtype, R, N, M):
     drift = (((y.double() - ref) * ref).sum() / (ref * ref).sum()).item()
     u = torch.finfo(dtype).eps / 2
     assert abs(drift) <= 1024 * 2.0 ** -23 + 4 * u / (R * M) ** 0.5 + 2.0 ** -18
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [1, 12, 30])
+@pytest.mark.parametrize("group", [32, 64, 128, 96, 384])
+def test_an_infinite_last_scale_stays_an_infinity(cuda_device, dtype, M, group):
+    # rows that end inside a step: what lies behind their end is no part of the last group
+    R, N = 8200, 4136
+    g = torch.Generator(device=cuda_device).manual_seed(group)
+    codes = torch.randint(0, 16, (R, N), generator=g, device=cuda_device, dtype=torch.uint8)
+    C = torch.rand((R, 16), generator=g, device=cuda_device) + 0.5
+    x = ((torch.rand((M, N), generator=g, device=cuda_device) + 0.5) / 64).to(dtype)
+    s = torch.rand((R, -(-N // group)), generator=g, device=cuda_device) + 0.5
+    s[5::7, -1] = float("inf")
+    y = km.km_matvec4(x, km.km_pack4(codes), C, s, group)
+    torch.cuda.synchronize()
+    want = torch.zeros(R, dtype=torch.bool, device=cuda_device)
+    want[5::7] = True
+    assert (torch.isposinf(y) == want[None]).all() and torch.isfinite(y[:, ~want]).all()
