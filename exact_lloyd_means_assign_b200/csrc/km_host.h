@@ -12,6 +12,12 @@
 
 #include "kmeans_b200.h"
 
+// Test-only switch of the codebook operators (km_debug_inject(3)): handed to their kernels as a parameter, so that
+// it costs nothing where it is off.
+namespace km {
+inline std::atomic<int> g_withhold{0};
+}  // namespace km
+
 // The device error word and the wait limit of km_common.cuh exist once per translation unit; the
 // other units that wait export theirs for km_device_error and km_debug_wait_limit.
 namespace km {

@@ -1673,10 +1673,11 @@ km_status km_debug_wait_limit(unsigned long long limit_ns, unsigned long long *p
 }
 
 km_status km_debug_inject(int mode) {
-    if (mode < 0 || mode > 2) return KM_ERR_INVALID_ARG;
+    if (mode < 0 || mode > 3) return KM_ERR_INVALID_ARG;
     if (cudaDeviceSynchronize() != cudaSuccess ||
         cudaMemcpyToSymbol(km::g_km_inject, &mode, sizeof(mode)) != cudaSuccess)
         return KM_ERR_CUDA;
+    km::g_withhold = mode == 3 ? 1 : 0;
     return KM_OK;
 }
 

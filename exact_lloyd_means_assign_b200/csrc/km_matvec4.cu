@@ -164,6 +164,7 @@ struct MmaParams {
     int N, K, ngroups;
     int rtiles, items;           // tiles of 16 rows, times tiles of 8 NT tokens
     FastDiv cpg;                 // 32-code chunks per scale group
+    int withhold;                // test only: the first half block never asks for its first stage
 };
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             const int row = (item % p.rtiles) * 16;
             for (int s = 0; s < nstages; ++s) {
                 if (!mbar_wait_warp(empty0 + 8 * slot, ph, abortp)) { item = p.items - step; break; }
-                if (lane == 0) {
+                if (lane == 0 && !(p.withhold && asked == 0 && blockIdx.x == 0 && half == 0)) {
                     mbar_arrive_expect_tx(full0 + 8 * slot, kStageBytes);
 #pragma unroll
                     for (int i = 0; i < kStageRow / 128; ++i)
@@ -631,6 +632,7 @@ km_status tc_launch(const uint8_t *packed, const T *x, TcMvParams p, T *y, cudaS
     static std::atomic<uint64_t> ready{0};
     if (!allow_smem(kernel, smem, ready)) return KM_ERR_CUDA;
     p.idesc = km::mma_idesc_f16(bf16 ? 1u : 0u, kTcRows, NTOK);
+    p.withhold = km::g_withhold;
     p.rtiles = static_cast<int>(ceil_div(p.R, kTcRows));
     p.mtiles = static_cast<int>(ceil_div(p.M, NTOK));
     p.steps = static_cast<int>(ceil_div(p.N, L::kStep));
@@ -705,6 +707,7 @@ km_status matvec4_mma(const void *xv, int64_t M, const uint8_t *packed, const fl
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return KM_ERR_CUDA;
     MmaParams p = {};
+    p.withhold = km::g_withhold;
     p.C = C;
     p.scales = scales;
     p.pitch = pitch_of(N);

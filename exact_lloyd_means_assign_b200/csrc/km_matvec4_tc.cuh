@@ -73,6 +73,7 @@ struct TcMvParams {
     int x3d, svec;                 // tokens by one copy per step; rows of scales on 16-byte boundaries
     FastDiv cpg;                   // 32-code chunks per scale group
     uint32_t idesc;
+    int withhold;                  // test only: the first block never asks for its first step
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
             for (int s = st0; s < st1; ++s) {
                 if (!mbar_ready(EMPTY(slot), ph, abortp)) { ok = false; break; }
-                if (lane == 0) {
+                if (lane == 0 && !(p.withhold && g == 0 && blockIdx.x == 0)) {
                     const uint32_t dst = stage_addr(slot);
                     mbar_arrive_expect_tx(FULL(slot), L::kStage);
                     tma_load_2d(dst, &tmW, FULL(slot), s * (STEP / 2), r0, pol);

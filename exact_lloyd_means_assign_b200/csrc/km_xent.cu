@@ -234,6 +234,7 @@ km_status tc_launch(const Operand &A, const Operand &Bo, int64_t B, int64_t M, i
     p.idesc = km::mma_idesc_f16(bf16 ? 1u : 0u, 2 * TBM, TBN) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
               (MODE != kOut && e.scale < 0.f ? 1u << 13 : 0u);   // bit 13 negates A
     p.vec = N % 8 == 0 && (!e.outT || aligned(e.outT, 16)) ? 1 : 0;
+    p.withhold = km::g_withhold;
     e.splits = static_cast<int>(splits);
     const int64_t items = static_cast<int64_t>(p.mt) * p.nt * splits * B;
     if (items > kMaxIndex) return KM_ERR_UNSUPPORTED;
@@ -349,6 +350,7 @@ km_status fused_launch(const void *A, const void *Bo, int64_t B, int64_t M, int6
     p.rows = w.rows;
     p.wmax = w.wmax;
     p.pscale = pscale;
+    p.withhold = km::g_withhold;
     p.parts = w.parts;
     p.out = out;
     p.vec = d % 8 == 0 && aligned(out, 16) ? 1 : 0;

@@ -91,6 +91,7 @@ struct FParams {
     const PointRow *rows;     // [batches][tiles of points][128] (dX)
     const unsigned int *wmax;
     float pscale;
+    int withhold;             // test only: the first block never asks for its first tile
     float *parts;             // [blocks][2][128][DN]: a block's first and last row tile, where shared
     void *out;
     int vec;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             __syncwarp();
             for (; j < je; ++j) {
                 if (!mbar_wait_warp(B_EMPTY(slot), ph, abortp)) { ok = false; break; }
-                if (lane == 0) {
+                if (lane == 0 && !(p.withhold && uses == 0 && blockIdx.x == 0)) {
                     const uint32_t dst = ring + slot * Sh::kStage;
                     mbar_arrive_expect_tx(B_FULL(slot), Sh::kTile + (COL ? static_cast<uint32_t>(sizeof(PointTile)) : 0u));
 #pragma unroll

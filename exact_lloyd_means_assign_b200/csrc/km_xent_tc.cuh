@@ -62,6 +62,7 @@ struct TcParams {
     int Kk;
     uint32_t idesc;
     int vec;              // rows of the output start on 16-byte boundaries
+    int withhold;         // test only: the first pair never asks for its first stage
     FastDiv div_batch, div_split, div_group, div_last;   // items per batch, per split, per group of
                                                          // row tiles; row tiles of the last group
 };
@@ -181,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
             const int kc1 = min(p.kchunks, (it.split + 1) * p.kper);
             for (int kc = it.split * p.kper; kc < kc1; ++kc) {
                 if (!mbar_wait_warp(EMPTY(stage), ph ^ 1u, abortp)) { ok = false; break; }
-                if (lane == 0) {
+                if (lane == 0 && !(p.withhold && uses == 0 && blockIdx.x < 2)) {
                     if (leader) mbar_arrive_expect_tx(FULL(stage), 2 * Sh::kStage);
                     const uint32_t a = sbase + stage * Sh::kStage, bsm = a + Sh::kA;
                     const uint32_t bar = map_to_rank(FULL(stage), 0);

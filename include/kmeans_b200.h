@@ -270,8 +270,10 @@ km_status km_device_error(void *stream, int *code);
  * are left unwritten. km_debug_inject(2) makes the first CTA of the next single-launch small fits
  * (km_fit on shapes with K * d <= 4096, d <= 64 and at most 2048 CTAs of 256 points) skip its
  * first grid-barrier arrival: the other CTAs' waits run out, set bit 0 and an abort word, and
- * every CTA leaves. km_debug_inject(0) (the default) turns both off. Both calls synchronise the
- * device first. No fault, trap or endless loop is involved.
+ * every CTA leaves. km_debug_inject(3) makes the next tensor-core kernels of km_matvec4, km_xent and
+ * km_xent_grad withhold the first stage of their first block (or SM pair): its roles leave in the same way,
+ * and its results are left unwritten or incomplete. km_debug_inject(0) (the default) turns all off. Both calls
+ * synchronise the device first. No fault, trap or endless loop is involved.
  */
 km_status km_debug_wait_limit(unsigned long long limit_ns, unsigned long long *previous_ns);
 km_status km_debug_inject(int mode);
