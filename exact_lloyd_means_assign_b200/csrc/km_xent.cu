@@ -71,6 +71,10 @@ inline bool use_tc(km_dtype dt, int64_t d, float scale, const void *X, const voi
     return dt != KM_F32 && scale != 0.f && (d % 8 != 0 || (aligned(X, 16) && aligned(C, 16))) && encode_fn() != nullptr;
 }
 
+// A logit is one chain of truncating additions (loss at d = 1024, 8192 and 65536 off by 5e-7, 4e-6 and 4e-5 of itself,
+// in terms of both signs): rows of more than kMaxChain products are summed on the CUDA cores, rounded to nearest.
+inline bool logits_on_tc(int64_t d) { return d <= kMaxChain * 16; }
+
 struct LossWs {
     float2 *pairs;
     float *zt;
@@ -300,7 +304,7 @@ km_status copy_rows(const void *src, const int32_t *ids, int64_t rows, int64_t d
 template <typename T>
 km_status loss_typed(const void *X, km_dtype dt, const void *C, const int32_t *ids, int64_t B, int64_t N, int64_t K,
                      int64_t d, float scale, float *loss, float *lse, const LossWs &w, cudaStream_t st) {
-    const bool tc = use_tc(dt, d, scale, X, C);
+    const bool tc = use_tc(dt, d, scale, X, C) && logits_on_tc(d);
     const int64_t dp = tc ? padded(d, dt) : d;
     km_status s;
     if (dp != d) {
@@ -458,7 +462,7 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
         p.ldp = kc;
         p.wmax = wmax;
         p.pscale = pscale;
-        s = product<T, kProb>(tc, Operand{X, N * dp, dp, 1}, Operand{Ck, K * dp, dp, 1}, B, N, kn, dp, p, 1, st);
+        s = product<T, kProb>(tc && logits_on_tc(d), Operand{X, N * dp, dp, 1}, Operand{Ck, K * dp, dp, 1}, B, N, kn, dp, p, 1, st);
         if (s != KM_OK) return s;
         if (dX) {
             Epi q = {};

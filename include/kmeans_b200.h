@@ -437,6 +437,9 @@ km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int
  *     z[n,k] = scale * <X[b,n], C[b,k]>,  lse[b,n] = log sum_k exp(z[n,k]),
  *     loss[b,n] = lse[b,n] - z[n, ids[b,n]], 0 where ids[b,n] is outside [0,K) (no label).
  * X[B,N,d], C[B,K,d] in `dtype`; loss[B,N], lse[B,N] fp32 out, either may be NULL.
+ * Sums are fp32. The tensor cores, which take 16-bit rows of up to 16384 values, truncate where they add: a logit
+ * is off by up to 2^-23 of its running sum for every 16 products (measured: the loss by 5e-7 of itself at
+ * d = 1024, 4e-6 at 8192). Longer rows are summed on the CUDA cores.
  * A table row may be masked by a coordinate that brings its logits to minus infinity or far below the
  * others, the type's lowest value included: it adds nothing to lse. With every logit minus infinity lse is
  * minus infinity; a logit of plus infinity gives NaN.

@@ -279,3 +279,30 @@ def test_small_probabilities_keep_their_bits_in_fp16(cuda_device):
         got, ref = dC[0, live:].double(), rC[live:]
         assert ((got - ref).norm() / ref.norm()).item() <= 2 * 2.0 ** -11
         assert ((got - ref).abs() <= 2.0 ** -10 * ref.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [16384, 16392, 65536, 65541])
+def test_logits_of_very_long_rows_do_not_drift(cuda_device, dtype, d):
+    # all products positive, one table row: lse is the logit. At most 1024 truncated additions, 2^-23 of the sum
+    # each, or d rounded ones, whose errors of 2^-24 have both signs (4 sqrt(d) of them)
+    g = torch.Generator(device=cuda_device).manual_seed(d)
+    X = (torch.rand((1, 70, d), generator=g, device=cuda_device) + 0.5).to(dtype)
+    C = (torch.rand((1, 1, d), generator=g, device=cuda_device) + 0.5).to(dtype)
+    ids = torch.zeros((1, 70), dtype=torch.int32, device=cuda_device)
+    loss, lse = km.km_xent(X, C, ids, 2.0 ** -10)
+    ref = (X[0].double() @ C[0, 0].double()) * 2.0 ** -10
+    assert ((lse[0] - ref).abs() <= (1024 * 2.0 ** -23 + 4 * d ** 0.5 * 2.0 ** -24) * ref).all()
+    assert (loss.abs() <= 2.0 ** -22 * ref).all()
+    C2 = torch.cat([C * 0, C], 1).contiguous()
+    loss, lse = km.km_xent(X, C2, ids, 2.0 ** -13)
+    dX, dC = km.km_xent_grad(X, C2, ids, lse, None, 2.0 ** -13)
+    torch.cuda.synchronize()
+    assert km.km_device_error() == 0
+    rl, rs, rX, rC = _fp64(X[0], C2[0], ids[0], torch.ones(70, device=cuda_device), 2.0 ** -13)
+    u = torch.finfo(dtype).eps / 2
+    assert (loss[0] - rl).abs().max() <= 2 * MAX_DRIFT * rs.max() + 2.0 ** -20
+    # (P by half a step, with an exponent off by the logit's drift; the result by half a step or fp16's subnormal one)
+    for got, ref in ((dX[0], rX), (dC[0], rC)):
+        floor = 2.0 ** -25 if dtype == torch.float16 else 0.0
+        assert ((got.double() - ref).abs() <= (2.1 * u + 4 * MAX_DRIFT * rs.max()) * ref.abs() + 70 * floor).all()
