@@ -107,6 +107,11 @@ __device__ __forceinline__ uint32_t fd_div(const FastDiv &f, uint32_t n) {
     return (__umulhi(f.m, n) + n) >> f.s;
 }
 
+// The same for numerators that may be larger, by a division where they are.
+__device__ __forceinline__ int64_t fd_div64(const FastDiv &f, int64_t n) {
+    return n < (int64_t{1} << 31) ? static_cast<int64_t>(fd_div(f, static_cast<uint32_t>(n))) : n / f.d;
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

@@ -117,7 +117,7 @@ inline FusedWs carve_fused(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d
     f.X = c.take<uint8_t>(static_cast<size_t>(B * N * dp) * 2);
     f.C = c.take<uint8_t>(static_cast<size_t>(B * K * dp) * 2);
     f.w = c.take<float>(static_cast<size_t>(B * N) * 4);
-    f.wmax = c.take<unsigned int>(4);
+    f.wmax = c.take<unsigned int>(kStats * 4);
     f.points = c.take<PointTile>(static_cast<size_t>(B * f.ptiles) * sizeof(PointTile));
     f.rows = c.take<PointRow>(static_cast<size_t>(B * f.ptiles) * FR * sizeof(PointRow));
     f.parts = c.take<float>(static_cast<size_t>(fused_blocks(fused_tiles(B, N, K))) * 2 * FR * (d > 64 ? 128 : 64) * 4);
@@ -126,6 +126,7 @@ inline FusedWs carve_fused(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d
 
 struct GradWs {
     void *P, *X, *C;
+    void *Xs;       // (fp16) the points as dC sums them, where X is a padded copy already
     float *w, *parts, *dxacc;
     unsigned int *wmax;
 };
@@ -136,8 +137,9 @@ inline GradWs carve_grad(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d, 
     const int64_t dp = padded(d, dt);
     g.X = c.take<uint8_t>(static_cast<size_t>(B * N * dp) * dtype_size(dt));
     g.C = dp != d ? c.take<uint8_t>(static_cast<size_t>(B * K * dp) * 2) : nullptr;
+    g.Xs = dp != d && dt == KM_F16 ? c.take<uint8_t>(static_cast<size_t>(B * N * dp) * 2) : g.X;
     g.w = c.take<float>(static_cast<size_t>(B * N) * 4);
-    g.wmax = c.take<unsigned int>(4);
+    g.wmax = c.take<unsigned int>(kStats * 4);
     int64_t parts = 0;
     for (int64_t k0 = 0; k0 < K; k0 += kc) {
         const int64_t kn = std::min(kc, K - k0);
@@ -282,7 +284,10 @@ km_status out_product(bool tc, km_dtype dt, const Operand &A, const Operand &Bo,
     q.outT = nullptr;
     km_status s = product<T, kOut>(tc, A, Bo, B, M, N, Kk, q, splits, st);
     if (s != KM_OK) return s;
-    split_join_kernel<T><<<fill_blocks(B * M * N), 256, 0, st>>>(parts, static_cast<int>(splits), B * M * N, p);
+    const int64_t v = N % 4 == 0 && (!p.outT || aligned(p.outT, 4 * sizeof(T))) ? 4 : 1, units = B * M * N / v;
+    const km::FastDiv per_row = km::make_fastdiv(static_cast<uint32_t>(N / v));
+    auto kernel = v == 4 ? split_join_kernel<T, 4> : split_join_kernel<T, 1>;
+    kernel<<<fill_blocks(units), 256, 0, st>>>(parts, static_cast<int>(splits), units, per_row, p);
     return launch_status();
 }
 
@@ -400,9 +405,9 @@ km_status fused_grads(const void *X, km_dtype dt, const void *C, const int32_t *
     const int64_t dp = padded(d, dt);
     const float pscale = dt == KM_F16 ? 16384.f : 1.f;
     km_status s;
-    if (cudaMemsetAsync(w.wmax, 0, 4, st) != cudaSuccess) return KM_ERR_CUDA;
+    if (cudaMemsetAsync(w.wmax, 0, kStats * 4, st) != cudaSuccess) return KM_ERR_CUDA;
     km::xe::weight_kernel<<<static_cast<unsigned>(ceil_div(B * N, 256)), 256, 0, st>>>(
-        g, ids, B * N, static_cast<int>(K), scale, w.w, w.wmax);
+        g, ids, B * N, static_cast<int>(K), scale, w.w, w.wmax, false);
     if (launch_status() != KM_OK) return KM_ERR_CUDA;
     point_param_kernel<<<fill_blocks(B * w.ptiles * FR), 256, 0, st>>>(w.w, lse, ids, B, static_cast<int>(N), w.ptiles,
                                                                 static_cast<int>(K), w.wmax, pscale, w.points, w.rows);
@@ -434,12 +439,31 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
     km_status s;
     unsigned int *wmax = dt != KM_F32 ? w.wmax : nullptr;
     const float pscale = dt == KM_F16 ? 16384.f : 1.f;
-    if (wmax && cudaMemsetAsync(wmax, 0, 4, st) != cudaSuccess) return KM_ERR_CUDA;
+    if (wmax && cudaMemsetAsync(wmax, 0, kStats * 4, st) != cudaSuccess) return KM_ERR_CUDA;
     km::xe::weight_kernel<<<static_cast<unsigned>(ceil_div(B * N, 256)), 256, 0, st>>>(
-        g, ids, B * N, static_cast<int>(K), scale, w.w, wmax);
+        g, ids, B * N, static_cast<int>(K), scale, w.w, wmax, kShifts<T>);
     if (launch_status() != KM_OK) return KM_ERR_CUDA;
-    if (dC || dp != d) {
-        // points without a label become zeros here, so that nothing they hold reaches dC
+    // points without a label become zeros here, so that nothing they hold reaches dC
+    const void *Xc = w.X;         // the points as dC sums them
+    if constexpr (kShifts<T>) {
+        if (dC) {
+            Xc = w.Xs;
+            max_point_kernel<<<static_cast<unsigned>(std::min<int64_t>(B * N, 148 * 8)), 256, 0, st>>>(
+                static_cast<const __half *>(X), ids, B * N, static_cast<int>(d), static_cast<int>(K), wmax);
+            if (launch_status() != KM_OK) return KM_ERR_CUDA;
+            const bool whole = d % 8 == 0 && aligned(X, 16);
+            auto kernel = whole ? shift_points_kernel<8> : shift_points_kernel<1>;
+            const int64_t per = whole ? dp / 8 : dp;
+            kernel<<<fill_blocks(B * N * per), 256, 0, st>>>(
+                static_cast<const __half *>(X), ids, w.w, B * N, static_cast<int>(d),
+                km::make_fastdiv(static_cast<uint32_t>(per)), static_cast<int>(K), wmax, static_cast<__half *>(w.Xs));
+            if (launch_status() != KM_OK) return KM_ERR_CUDA;
+        }
+        if (dp != d) {
+            if ((s = copy_rows<T>(X, ids, B * N, d, dp, K, w.X, st)) != KM_OK) return s;
+            X = w.X;
+        }
+    } else if (dC || dp != d) {
         if ((s = copy_rows<T>(X, ids, B * N, d, dp, K, w.X, st)) != KM_OK) return s;
         X = w.X;
     }
@@ -468,6 +492,8 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
             Epi q = {};
             q.wmax = wmax;
             q.pscale = pscale;
+            q.rows = true;
+            q.w = w.w;
             q.acc = k0 ? w.dxacc : nullptr;
             if (k0 + kc < K) q.out32 = w.dxacc;
             else q.outT = dX;
@@ -485,7 +511,7 @@ km_status grad_typed(const void *X, km_dtype dt, const void *C, const int32_t *i
             for (int64_t b = 0; b < B; b += nb) {
                 q.outT = static_cast<T *>(dC) + (b * K + k0) * d;
                 s = out_product<T>(tc, dt, Operand{static_cast<const T *>(w.P) + b * N * kc, N * kc, 1, kc},
-                                   Operand{static_cast<const T *>(X) + b * N * dp, N * dp, 1, dp}, nb, kn, d, N, q,
+                                   Operand{static_cast<const T *>(Xc) + b * N * dp, N * dp, 1, dp}, nb, kn, d, N, q,
                                    w.parts, st);
                 if (s != KM_OK) return s;
             }

@@ -12,6 +12,8 @@
 // of up to 128 values keep P on the chip instead (km_xent_fused.cuh).
 #pragma once
 
+#include <type_traits>
+
 #include "km_common.cuh"
 
 namespace km {
@@ -35,8 +37,10 @@ struct Epi {
     void *P;               // [B, M, ldp]
     int64_t ldp;
     // kOut: out = acc (fp32) + value / f, or the fp32 partial of one split of the reduction
-    const unsigned int *wmax;   // bits of max |w| (16-bit points), or null
+    const unsigned int *wmax;   // bits of max |w| (16-bit points), and see Stat; or null
     float pscale;          // s of p_factor
+    bool rows;             // kOut, fp16: the result's rows are P's, whose shifts are undone (by the weights in w),
+                           // else the points' common one is
     const float *acc;      // added, or null
     float *out32;          // fp32 result or partials [split][B][M][N], or null
     void *outT;            // result in the points' type, or null
@@ -60,6 +64,27 @@ __device__ __forceinline__ float p_factor(const unsigned int *wmax, float s, boo
 // is infinite (every logit masked: the sum is then 0 instead of NaN).
 __device__ __forceinline__ float sum_base(float m) { return isinf(m) ? 0.f : m; }
 
+// fp16's range is too narrow for rows of P whose weights differ by many orders: beside a weight of 2^13, a row that
+// weighs 2^-13 would keep its label's entry alone. Every row of P is therefore multiplied by 2^h, which brings its
+// weight to the largest one's power of two; dX's rows are divided by it, and for dC, which sums over the points, the
+// points are: X 2^(q - h), with q bringing the largest of them to the top of fp16's range, so that those
+// divided by much keep their bits. All powers of two; with weights within a factor of two nothing changes.
+// (bf16 has fp32's range and needs none of it.)
+template <typename T> constexpr bool kShifts = std::is_same<T, __half>::value;
+enum Stat { kMaxW = 0, kMinW = 1, kMaxX = 2, kStats = 3 };      // bits of max |w|, ~bits of min |w| > 0, bits of max |x|
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+__device__ __forceinline__ int exponent_of(uint32_t bits) { return static_cast<int>(bits >> 23 & 255); }
+// max_exp: exponent_of the largest weight
+__device__ __forceinline__ int row_shift(int max_exp, float w) {
+    return w == 0.f ? 0 : min(24, max(0, max_exp - exponent_of(__float_as_uint(w))));
+}
+__device__ __forceinline__ bool any_shift(const unsigned int *stat) {
+    return stat[kMinW] != 0 && exponent_of(~stat[kMinW]) < exponent_of(stat[kMaxW]);
+}
+__device__ __forceinline__ int point_shift(const unsigned int *stat) {
+    return any_shift(stat) && stat[kMaxX] ? min(24, max(0, 14 + 127 - exponent_of(stat[kMaxX]))) : 0;
+}
+
 // Two fp32 values in one register pair, for the packed fp32 arithmetic of sm_100.
 __device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
     uint64_t r;
@@ -79,6 +104,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+
+// What undoes the shifts in row br of a result.
+__device__ __forceinline__ float out_shift(const Epi &p, int64_t br) {
+    return pow2f(p.rows ? -row_shift(exponent_of(p.wmax[kMaxW]), p.w[br]) : -point_shift(p.wmax));
+}
+
 // ------------------------------------------------------------------ CUDA-core products
 
 // One operand of a product: element (row, k) of batch b at base + b * batch + row * row_s + k * k_s,
@@ -226,7 +257,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
             if (!rin) continue;
             const int label = p.ids[br];
             const bool has = label >= 0 && label < p.K;
-            const float w = p.w[br] * fac, lse = p.lse[br];
+            const float w = p.w[br] * fac * (kShifts<T> ? pow2f(row_shift(exponent_of(p.wmax[kMaxW]), p.w[br])) : 1.f), lse = p.lse[br];
             T *Pr = static_cast<T *>(p.P) + br * p.ldp;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -238,6 +269,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
             }
         } else {
             if (!rin) continue;
+            const float back = kShifts<T> && p.splits == 1 ? out_shift(p, br) : 1.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int col = n0 + (j & 3) + tx * 4 + (j >> 2) * 64;
@@ -246,7 +278,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
                 if (p.splits > 1) {
                     p.out32[(split * nb * M) * N + at] = acc[i][j];
                 } else {
-                    const float v = acc[i][j] * inv + (p.acc ? p.acc[at] : 0.f);
+                    const float v = acc[i][j] * (inv * back) + (p.acc ? p.acc[at] : 0.f);
                     if (p.out32) p.out32[at] = v;
                     else static_cast<T *>(p.outT)[at] = Cvt<T>::from_f(v);
                 }
@@ -298,11 +330,11 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// w[b,n] = g[b,n] * scale, 0 without a label; with wmax the bits of max |w| (order of the atomics
-// does not matter to a maximum).
+// w[b,n] = g[b,n] * scale, 0 without a label; with wmax the bits of max |w| and, wanted, of min |w| > 0 (order of the
+// atomics does not matter to a maximum).
 __global__ void __launch_bounds__(256)
     weight_kernel(const float *__restrict__ g, const int32_t *__restrict__ ids, int64_t rows, int K, float scale,
-                  float *__restrict__ w, unsigned int *__restrict__ wmax) {
+                  float *__restrict__ w, unsigned int *__restrict__ wmax, bool want_min) {
     const int64_t i = blockIdx.x * 256ll + threadIdx.x;
     float v = 0.f;
     if (i < rows) {
@@ -313,7 +345,57 @@ __global__ void __launch_bounds__(256)
     if (wmax) {
         // (a weight that is not finite spoils its own terms only)
         const unsigned int m = __reduce_max_sync(0xffffffffu, isfinite(v) ? __float_as_uint(fabsf(v)) : 0u);
-        if ((threadIdx.x & 31) == 0 && m) atomicMax(wmax, m);
+        if ((threadIdx.x & 31) == 0 && m) atomicMax(wmax + kMaxW, m);
+        if (want_min) {
+            const unsigned int least = __reduce_max_sync(0xffffffffu, isfinite(v) && v != 0.f ? ~__float_as_uint(fabsf(v)) : 0u);
+            if ((threadIdx.x & 31) == 0 && least) atomicMax(wmax + kMinW, least);
+        }
+    }
+}
+
+// The largest |x| of the points with a label, infinities left out; only where weights differ at all.
+__global__ void __launch_bounds__(256)
+    max_point_kernel(const __half *__restrict__ X, const int32_t *__restrict__ ids, int64_t rows, int d, int K,
+                     unsigned int *__restrict__ stat) {
+    if (!any_shift(stat)) return;
+    uint32_t m = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int id = ids[r];
+        if (id < 0 || id >= K) continue;
+        for (int c = threadIdx.x; c < d; c += 256) {
+            const float v = fabsf(__half2float(X[r * d + c]));
+            if (v < INFINITY) m = max(m, __float_as_uint(v));
+        }
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0 && m) atomicMax(stat + kMaxX, m);
+}
+
+// The points as dC sums them: X 2^(q - h), rows without a label zeros; [rows, d] to rows of `per`
+// units of V values: eight, or one where rows are no whole 16-byte units.
+template <int V>
+__global__ void __launch_bounds__(256)
+    shift_points_kernel(const __half *__restrict__ X, const int32_t *__restrict__ ids, const float *__restrict__ w,
+                        int64_t rows, int d, FastDiv per, int K, const unsigned int *__restrict__ stat,
+                        __half *__restrict__ dst) {
+    struct alignas(2 * V) Unit {
+        __half v[V];
+    };
+    const int q = point_shift(stat), max_exp = exponent_of(stat[kMaxW]);
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < rows * per.d; i += gridDim.x * 256ll) {
+        const int64_t r = fd_div64(per, i);
+        const int c = static_cast<int>(i - r * per.d) * V, id = ids[r];
+        Unit u = {};
+        if (id >= 0 && id < K && c < d) {
+            u = *reinterpret_cast<const Unit *>(X + r * d + c);
+            const int e = q - row_shift(max_exp, w[r]);
+            if (e) {
+                const float f = pow2f(e);
+#pragma unroll
+                for (int k = 0; k < V; ++k) u.v[k] = __float2half_rn(__half2float(u.v[k]) * f);
+            }
+        }
+        reinterpret_cast<Unit *>(dst)[i] = u;
     }
 }
 
@@ -343,17 +425,36 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Joins the splits of a product in split order; adds acc, scales back, writes fp32 or T.
-template <typename T>
+// Joins the splits of a product in split order; adds acc, scales back, writes fp32 or T: V values at a time, of one
+// row (8192 x 256 in two splits, under the profiler: 12 us value by value, with a row's factor 15, four at a time 8).
+template <typename T, int V>
 __global__ void __launch_bounds__(256)
-    split_join_kernel(const float *__restrict__ parts, int splits, int64_t count, Epi p) {
+    split_join_kernel(const float *__restrict__ parts, int splits, int64_t units, FastDiv units_per_row, Epi p) {
+    struct alignas(4 * V) F {
+        float v[V];
+    };
+    struct alignas(sizeof(T) * V) O {
+        T v[V];
+    };
     const float inv = p_factor(p.wmax, p.pscale, true);
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
-        float v = 0.f;
-        for (int s = 0; s < splits; ++s) v += parts[s * count + i];
-        v = v * inv + (p.acc ? p.acc[i] : 0.f);
-        if (p.out32) p.out32[i] = v;
-        else static_cast<T *>(p.outT)[i] = Cvt<T>::from_f(v);
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < units; i += gridDim.x * 256ll) {
+        F s = {};
+        for (int k = 0; k < splits; ++k) {
+            const F x = reinterpret_cast<const F *>(parts)[k * units + i];
+#pragma unroll
+            for (int j = 0; j < V; ++j) s.v[j] += x.v[j];
+        }
+        const float f = inv * (kShifts<T> ? out_shift(p, p.rows ? fd_div64(units_per_row, i) : 0) : 1.f);
+        F a = {};
+        if (p.acc) a = reinterpret_cast<const F *>(p.acc)[i];
+        O o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s.v[j] = s.v[j] * f + a.v[j];
+            o.v[j] = Cvt<T>::from_f(s.v[j]);
+        }
+        if (p.out32) reinterpret_cast<F *>(p.out32)[i] = s;
+        else static_cast<O *>(p.outT)[i] = o;
     }
 }
 

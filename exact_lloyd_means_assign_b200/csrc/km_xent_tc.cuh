@@ -264,7 +264,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
         // overflow as the sums' base; their terms are 0 then.
         const float floor_ = -3e38f / fmaxf(s2, 1.f);
         const float fac = MODE == kProb ? p_factor(ep.wmax, ep.pscale, false) : 1.f;
-        const float inv = MODE == kOut && ep.splits == 1 ? p_factor(ep.wmax, ep.pscale, true) : 1.f;
+        const int max_exp = kShifts<T> && MODE != kLse ? exponent_of(ep.wmax[kMaxW]) : 0;
+        // (of dC too: its points' common shift)
+        const float inv = MODE == kOut && ep.splits == 1
+            ? p_factor(ep.wmax, ep.pscale, true) * (kShifts<T> && !ep.rows ? pow2f(-point_shift(ep.wmax)) : 1.f) : 1.f;
         const uint32_t obuf = sbase + Sh::kOutOff + (warp - T_EPI0) * 2 * kOutBuf;
         int buf = 0, ob = 0;
         uint32_t aph = 0;
@@ -276,16 +279,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
         auto read_row = [&](int t) {
             if (t >= total) return;
             next = tc_item(p, t);
-            if (MODE == kOut) return;
+            if (MODE == kOut && !(kShifts<T> && ep.rows)) return;
             const int row = next.m * (2 * TBM) + static_cast<int>(rank) * TBM + q * 32 + lane;
             id_n = -1;
             if (row < p.M) {
                 const int64_t br = static_cast<int64_t>(next.b) * p.M + row;
-                id_n = __ldg(ep.ids + br);
-                if (MODE == kProb) {
-                    w_n = __ldg(ep.w + br);
-                    lse_n = __ldg(ep.lse + br);
-                }
+                if (MODE != kOut) id_n = __ldg(ep.ids + br);
+                if (MODE != kLse) w_n = __ldg(ep.w + br);
+                if (MODE == kProb) lse_n = __ldg(ep.lse + br);
             }
         };
         read_row(t0);
@@ -295,6 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
             const int c0 = it.n * TBN + half * HALF;
             const bool rin = row < p.M;
             const int64_t br = static_cast<int64_t>(it.b) * p.M + row;
+            const float back = kShifts<T> && MODE == kOut && ep.rows ? inv * pow2f(-row_shift(max_exp, w_n)) : inv;
             int label = -1;
             // kProb: P = sign (2^(z log2e + off) - |w| [label]) with off = log2 |w| - lse log2e
             float aw = 0.f, off = 0.f;
@@ -303,7 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                 const bool has = id_n >= 0 && id_n < ep.K;
                 label = has ? id_n - ep.k0 : -1;
                 if (MODE == kProb) {
-                    const float w = has ? w_n * fac : 0.f;
+                    const float w = has ? w_n * fac * (kShifts<T> ? pow2f(row_shift(max_exp, w_n)) : 1.f) : 0.f;
                     aw = fabsf(w);
                     off = __log2f(aw) - lse_n * kLog2e;
                     sign = w < 0.f ? 0x80008000u : 0u;
@@ -439,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(T_THREADS, 1)
                         float f[32];
                         const bool whole = p.vec && col + 32 <= p.N;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * inv;
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * back;
                         if (ep.acc) {
                             if (whole) {
 #pragma unroll

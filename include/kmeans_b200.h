@@ -451,8 +451,9 @@ km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int
  * dC[B,K,d] in `dtype`, either may be NULL; they may not overlap the inputs. The logits are computed
  * again (16-bit rows of up to 128 values: tile by tile for each gradient, without scratch for P; else
  * one piece of the table at a time), and P is held in `dtype`, relative to the largest |g * scale|, for dX of
- * 16-bit rows of up to 128 values to the point's own (fp16: times 2^14, so that small probabilities keep
- * their bits; in two parts for tables of up to 128 rows of up to 128 values); all sums are fp32, in an order fixed
+ * 16-bit rows of up to 128 values to the point's own. (fp16: times 2^14, so that small probabilities keep
+ * their bits; rows of weights below the largest are moved up by powers of two, as far as 2^24, and for dC the
+ * points down instead.) Tables of up to 128 rows of up to 128 values hold P in two parts; all sums are fp32, in an order fixed
  * by the sizes and the number of SMs. Points without a label may hold any values: they reach neither
  * gradient (their own rows of dX are zero). An infinite value of the table makes dX NaN in its column, as
  * the formula has it (0 times infinity); dC stays as if the masked row were absent. To train with masked

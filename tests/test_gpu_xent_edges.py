@@ -157,7 +157,8 @@ def test_every_row_masked(cuda_device, dtype, d):
         assert ((lse.double() - low).abs() <= 2.0 ** -8 * abs(low) + 20).all()
 
 
-@pytest.mark.parametrize("d,N,K", [(64, 300, 700), (128, 500, 90), (100, 20000, 300)])
+@pytest.mark.parametrize("d,N,K", [(64, 300, 700), (128, 500, 90), (100, 20000, 300), (136, 300, 700), (201, 70, 2100), (512, 4000, 300),
+                                   (136, 70000, 2500)])
 @pytest.mark.parametrize("low", [-12, -22, -26])
 def test_rows_of_small_weight_beside_large_ones(cuda_device, d, N, K, low):
     # every second point weighs 2^low of the others; its row of dX is what it is alone: two roundings to half a
@@ -175,134 +176,53 @@ def test_rows_of_small_weight_beside_large_ones(cuda_device, d, N, K, low):
     # norm over a row's d values at most 2^-11 |p - label| |C|, the label's entry having no such error)
     assert (small - ref).norm() <= rounding.norm() + 2.0 ** -11 * ref.norm()
     assert ((small - ref).abs() <= 2 * rounding + 2.0 ** -11 * ref.norm(dim=1, keepdim=True) * 4 / d ** 0.5).all()
-    # and equal bits whatever the others weigh
+    # and equal bits whatever the others weigh (long rows: as far as 2^24 below the largest)
     g2 = g.clone()
     g2[0, ::2] = 2.0 ** (13 + low)
     alone, _ = km.km_xent_grad(X, C, ids, lse, g2)
-    assert torch.equal(alone[0, 1::2], dX[0, 1::2])
+    if d <= 128 or low >= -24:
+        assert torch.equal(alone[0, 1::2], dX[0, 1::2])
+    # dC sums over all of them. An entry of P is off by half a step (and by an exponent's 2^-18), which may fall together
+    # over the points; so may 2^-36 of the largest terms, those of a weight of 2^13 (an entry of P holds 14 bits below
+    # its row's weight and 10 more, a point of up to 2^3 lies 2^11 below fp16's top)
+    tC = torch.zeros_like(rC)
+    for n in range(0, N, 8192):
+        sl = slice(n, n + 8192)
+        p = torch.softmax(X[0, sl].double() @ C[0].double().t(), 1)
+        ok = (ids[0, sl] >= 0) & (ids[0, sl] < K)
+        p[ok, ids[0, sl][ok].long()] -= 1
+        p = p.abs() * torch.where(ok, g[0, sl], torch.zeros_like(g[0, sl]))[:, None]
+        p += 2.0 ** (13 - 36 + 11) * ok[:, None]
+        tC += p.t() @ X[0, sl].double().abs()
+    tC = tC * (2.0 ** -11 + 2.0 ** -18 + (1024 + N / 8192) * 2.0 ** -23) + 2.0 ** -11 * rC.abs() + 2.0 ** -25
+    # (results beyond fp16's largest number, 65504, are infinite)
+    fits, beyond = rC.abs() + tC < 65504, rC.abs() - tC > 65536
+    over = ((dC[0].double() - rC).abs() - tC)[fits]
+    assert (over <= 0).all(), (over.max().item(), (over > 0).sum().item())
+    assert (dC[0].double()[beyond] == torch.sign(rC[beyond]) * float("inf")).all()
 
 
-@pytest.mark.parametrize("dtype,d", [(torch.float16, 136), (torch.bfloat16, 200), (torch.float16, 130), (torch.float32, 40),
-                                     (torch.float16, 72)])
-def test_guards_streams_capture_and_unaligned_rows(cuda_device, dtype, d):
-    B, N, K = 2, 300, 700
-    X, C, ids, g = _inputs(B, N, K, d, dtype, cuda_device, seed=d)
-    loss, lse = km.km_xent(X, C, ids, 0.5)
-    dX, dC = km.km_xent_grad(X, C, ids, lse, g, 0.5)
-
-    def off(t):
-        # one element off every vector boundary, between guard values
-        buf = torch.full((t.numel() + 2,), 7.0, dtype=t.dtype, device=t.device)
-        buf[1:-1].copy_(t.flatten())
-        return buf, buf[1:-1].view(t.shape)
-    for x_off, c_off in ((True, True), (True, False), (False, True)):
-        X1, C1 = off(X)[1] if x_off else X, off(C)[1] if c_off else C
-        bx, dX1 = off(torch.zeros_like(dX))
-        bc, dC1 = off(torch.zeros_like(dC))
-        l1, s1 = km.km_xent(X1, C1, ids, 0.5)
-        km.km_xent_grad(X1, C1, ids, s1, g, 0.5, dX=dX1, dC=dC1)
-        torch.cuda.synchronize()
-        _check_loss(X, C, ids, 0.5, l1, s1)
-        _check_grad(X, C, ids, g, 0.5, dX1, dC1)
-        for b in (bx, bc):
-            assert b[0] == 7 and b[-1] == 7
-    lib, dt = km._load(), km._dt(dtype)
-    n1, n2 = lib.km_xent_workspace_size(B, N, K, d, dt), lib.km_xent_grad_workspace_size(B, N, K, d, dt)
-    w1 = torch.full((n1 + 4096,), 0xFF, dtype=torch.uint8, device=cuda_device)
-    w2 = torch.full((n2 + 4096,), 0xFF, dtype=torch.uint8, device=cuda_device)
-    l2, s2 = km.km_xent(X, C, ids, 0.5, ws=w1[:n1])
-    x2, c2 = km.km_xent_grad(X, C, ids, s2, g, 0.5, ws=w2[:n2])
+@pytest.mark.parametrize("scale_x", [1.0, 2.0 ** -12, 2.0 ** 9])
+@pytest.mark.parametrize("d", [64, 136])
+def test_table_rows_of_small_weights_alone(cuda_device, d, scale_x):
+    # the labels of the light points are rows that no heavy point has, and whose probabilities under the heavy ones
+    # vanish: what these rows of dC hold comes from weights of 2^-12 of the largest
+    N, K = 400, 300
+    gen = torch.Generator(device=cuda_device).manual_seed(d)
+    X = (torch.randn((N, d), generator=gen, device=cuda_device) * scale_x).half()
+    C = (torch.randn((K, d), generator=gen, device=cuda_device) * (2 / d ** 0.5)).half()
+    light = torch.arange(N, device=cuda_device) % 2 == 1
+    X[:, -1] = torch.where(light, -4.0, 4.0) * scale_x
+    C[:, -1] = torch.where(torch.arange(K, device=cuda_device) < 150, 6.0, -6.0).half()
+    ids = torch.where(light, 150 + torch.arange(N, device=cuda_device) % 150, torch.arange(N, device=cuda_device) % 150).to(torch.int32)
+    g = torch.where(light, 1.0 / 4, 1024.0).float() / scale_x
+    scale = 1 / scale_x
+    _, lse = km.km_xent(X[None], C[None], ids[None], scale)
+    dX, dC = km.km_xent_grad(X[None], C[None], ids[None], lse, (g * scale_x)[None], scale)
     torch.cuda.synchronize()
-    assert torch.equal(l2, loss) and torch.equal(x2, dX) and torch.equal(c2, dC)
-    assert (w1[n1:] == 0xFF).all() and (w2[n2:] == 0xFF).all()
-    side = torch.cuda.Stream()
-    side.wait_stream(torch.cuda.current_stream())
-    l3, s3 = km.km_xent(X, C, ids, 0.5, stream=side)
-    x3, c3 = km.km_xent_grad(X, C, ids, s3, g, 0.5, stream=side)
-    torch.cuda.synchronize()
-    assert torch.equal(l3, loss) and torch.equal(x3, dX) and torch.equal(c3, dC)
-    Xs, lo, ls, gx, gc = X.clone(), torch.empty_like(loss), torch.empty_like(lse), torch.empty_like(dX), torch.empty_like(dC)
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        km.km_xent(Xs, C, ids, 0.5, loss=lo, lse=ls, ws=w1[:n1])
-        km.km_xent_grad(Xs, C, ids, ls, g, 0.5, dX=gx, dC=gc, ws=w2[:n2])
-    for k in (1.0, 0.5):
-        Xs.copy_(X * k)
-        graph.replay()
-        torch.cuda.synchronize()
-        rl, rs = km.km_xent(X * k, C, ids, 0.5)
-        rx, rc = km.km_xent_grad(X * k, C, ids, rs, g, 0.5)
-        assert torch.equal(lo, rl) and torch.equal(gx, rx) and torch.equal(gc, rc)
-
-
-@pytest.mark.parametrize("dtype,B,N,K,d", [(torch.bfloat16, 2, 32768, 5000, 136), (torch.float16, 3, 20000, 4600, 200),
-                                           (torch.float32, 2, 40000, 4000, 24)])
-def test_batches_whose_table_comes_in_pieces(cuda_device, dtype, B, N, K, d):
-    # more entries of P than are held at a time: several pieces of the table, and dC by batch
-    X, C, ids, g = _inputs(B, N, K, d, dtype, cuda_device, seed=N)
-    loss, lse = km.km_xent(X, C, ids)
-    dX, dC = km.km_xent_grad(X, C, ids, lse, g)
-    torch.cuda.synchronize()
-    assert km.km_device_error() == 0
-    u = torch.finfo(dtype).eps / 2
-    for b in range(B):
-        rl, rs, rX, rC = _fp64(X[b], C[b], ids[b], g[b])
-        assert (lse[b] - rs).abs().max() < 2e-5 and (loss[b] - rl).abs().max() < 4e-5
-        # relative norms: half a step of P and of the result at most, plus fp32 sums; fp16 results near its
-        # subnormals half a step of those each
-        for got, ref in ((dX[b], rX), (dC[b], rC)):
-            floor = (2.0 ** -25 * ref.numel() ** 0.5 / ref.norm()).item() if dtype == torch.float16 else 0.0
-            assert ((got.double() - ref).norm() / ref.norm()).item() < 2 * u + 2e-5 + floor
-
-
-def test_small_probabilities_keep_their_bits_in_fp16(cuda_device):
-    # table rows that no point has as its label, and points of equal weight: dC of such a row is a sum of
-    # probabilities near 2^-22 times that weight alone. Held as they are they would lie among fp16's subnormals
-    # (steps of 2^-24: errors of 2^-4 each, 2^-9 and more in a row's sum over 1024 points); times 2^14 they keep all
-    # their bits, half a step u = 2^-11 each, and the result is rounded by half a step once more.
-    N, K, d, live = 1024, 3000, 64, 20
-    for d in (64, 136):
-        gen = torch.Generator(device=cuda_device).manual_seed(d)
-        X = torch.rand((N, d), generator=gen, device=cuda_device).half() + 0.5
-        C = torch.rand((K, d), generator=gen, device=cuda_device).half() * (4 / d)
-        X[:, -1] = 1
-        C[:, -1] = -8.0
-        C[:live, -1] = 4.0                       # the labelled rows take almost all of the softmax
-        ids = torch.randint(0, live, (1, N), generator=gen, device=cuda_device, dtype=torch.int32)
-        g = torch.full((1, N), 1024.0, device=cuda_device)
-        _, lse = km.km_xent(X[None], C[None], ids)
-        _, dC = km.km_xent_grad(X[None], C[None], ids, lse, g, want_dX=False)
-        torch.cuda.synchronize()
-        _, _, _, rC = _fp64(X, C, ids[0], g[0])
-        p = rC[live:].abs().max() / (1024 * N)
-        assert 2.0 ** -24 < p < 2.0 ** -18, p
-        got, ref = dC[0, live:].double(), rC[live:]
-        assert ((got - ref).norm() / ref.norm()).item() <= 2 * 2.0 ** -11
-        assert ((got - ref).abs() <= 2.0 ** -10 * ref.abs()).all()
-
-
-@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
-@pytest.mark.parametrize("d", [16384, 16392, 65536, 65541])
-def test_logits_of_very_long_rows_do_not_drift(cuda_device, dtype, d):
-    # all products positive, one table row: lse is the logit. At most 1024 truncated additions, 2^-23 of the sum
-    # each, or d rounded ones, whose errors of 2^-24 have both signs (4 sqrt(d) of them)
-    g = torch.Generator(device=cuda_device).manual_seed(d)
-    X = (torch.rand((1, 70, d), generator=g, device=cuda_device) + 0.5).to(dtype)
-    C = (torch.rand((1, 1, d), generator=g, device=cuda_device) + 0.5).to(dtype)
-    ids = torch.zeros((1, 70), dtype=torch.int32, device=cuda_device)
-    loss, lse = km.km_xent(X, C, ids, 2.0 ** -10)
-    ref = (X[0].double() @ C[0, 0].double()) * 2.0 ** -10
-    assert ((lse[0] - ref).abs() <= (1024 * 2.0 ** -23 + 4 * d ** 0.5 * 2.0 ** -24) * ref).all()
-    assert (loss.abs() <= 2.0 ** -22 * ref).all()
-    C2 = torch.cat([C * 0, C], 1).contiguous()
-    loss, lse = km.km_xent(X, C2, ids, 2.0 ** -13)
-    dX, dC = km.km_xent_grad(X, C2, ids, lse, None, 2.0 ** -13)
-    torch.cuda.synchronize()
-    assert km.km_device_error() == 0
-    rl, rs, rX, rC = _fp64(X[0], C2[0], ids[0], torch.ones(70, device=cuda_device), 2.0 ** -13)
-    u = torch.finfo(dtype).eps / 2
-    assert (loss[0] - rl).abs().max() <= 2 * MAX_DRIFT * rs.max() + 2.0 ** -20
-    # (P by half a step, with an exponent off by the logit's drift; the result by half a step or fp16's subnormal one)
-    for got, ref in ((dX[0], rX), (dC[0], rC)):
-        floor = 2.0 ** -25 if dtype == torch.float16 else 0.0
-        assert ((got.double() - ref).abs() <= (2.1 * u + 4 * MAX_DRIFT * rs.max()) * ref.abs() + 70 * floor).all()
+    _, _, rX, rC = _fp64(X, C, ids, g * scale_x, scale)
+    # (roundings of P and of the result, half a step each, in the norm of the light rows; fp16's subnormals)
+    ref, got = rC[150:], dC[0, 150:].double()
+    assert (got - ref).norm() <= 2 * 2.0 ** -11 * ref.norm() + 2.0 ** -25 * ref.numel() ** 0.5
+    ref, got = rX[light], dX[0][light].double()
+    assert (got - ref).norm() <= 2 * 2.0 ** -11 * ref.norm() + 2.0 ** -25 * ref.numel() ** 0.5
