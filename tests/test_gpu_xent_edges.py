@@ -226,3 +226,25 @@ def test_table_rows_of_small_weights_alone(cuda_device, d, scale_x):
     assert (got - ref).norm() <= 2 * 2.0 ** -11 * ref.norm() + 2.0 ** -25 * ref.numel() ** 0.5
     ref, got = rX[light], dX[0][light].double()
     assert (got - ref).norm() <= 2 * 2.0 ** -11 * ref.norm() + 2.0 ** -25 * ref.numel() ** 0.5
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d,K", [(136, 260), (201, 300), (72, 90)])
+def test_points_without_labels_of_other_forms_may_hold_anything(cuda_device, dtype, d, K):
+    # long rows, padded ones, and few table rows, with weights that differ by many orders
+    X, C, ids, g = _inputs(2, 150, K, d, dtype, cuda_device, seed=d)
+    g = g * torch.where(torch.arange(150, device=cuda_device) % 3 == 0, 2.0 ** -9, 1.0)[None]
+    bad = (ids < 0) | (ids >= K)
+    assert bad.any()
+    X[bad] = 0
+    _, lse = km.km_xent(X, C, ids)
+    dX0, dC0 = km.km_xent_grad(X, C, ids, lse, g)
+    for fill in (float("nan"), float("inf"), 6e4):
+        X2, g2 = X.clone(), g.clone()
+        X2[bad] = fill
+        g2[bad] = fill
+        loss, lse2 = km.km_xent(X2, C, ids)
+        dX, dC = km.km_xent_grad(X2, C, ids, lse2, g2)
+        torch.cuda.synchronize()
+        assert (loss[bad] == 0).all() and torch.isfinite(loss).all()
+        assert torch.equal(dX, dX0) and torch.equal(dC, dC0)
