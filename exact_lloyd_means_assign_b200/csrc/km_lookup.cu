@@ -911,7 +911,7 @@ inline SortPlan sort_plan(int64_t B, int64_t N, int64_t K) {
     return p;
 }
 
-// Entries per range: as many ranges as fill the device with their groups (32 per SM on 148 SMs), at
+// Entries per range: as many ranges as fill the device with their groups (64 per SM on 148 SMs), at
 // least 16 entries each.
 inline int64_t grad_range(int64_t T) { return std::max<int64_t>(16, ceil_div(T, 148 * 64)); }
 

@@ -126,10 +126,11 @@ __global__ void __launch_bounds__(32 * kSimtWarps)
 // ------------------------------------------------------------------ 16-bit tokens: mma form
 //
 // Tiles of 16 rows of weights. The product runs as m16n8k16 matrix instructions with the weights
-// as the row operand, so eight tokens cost what one costs. What bounds it: an instruction takes a
-// sub-partition 32 cycles for its 256 weights (30 us for 32768 x 8192, where the bytes would take 22 and
-// the lookups 15), and the tables are built anew for every tile. Measured: 32768 x 8192, one token, a scale
-// per 128 weights 47 us, 3.1 TB/s; 4096 x 4096 5.7 us. Turning codes into operands takes one
+// as the row operand, so eight tokens cost what one costs. What bounds it: the lookups and the latencies around
+// them. At 32768 x 8192, one token, a scale per 128 weights, the profile has shared memory's wavefronts 63 % busy,
+// the fullest pipe, the tensor pipe 15 %, and short scoreboard, fixed waits and long scoreboard as the stalls; the
+// tables are built anew for every tile. Measured there: 47 us, 3.1 TB/s (the bytes would take 22); 4096 x 4096
+// 5.7 us. Turning codes into operands takes one
 // shared-memory read per pair of codes: a byte indexes a 256-entry table of value pairs. A table
 // row is 256 bytes, one word per lane and row half, so every lane reads its own bank (lane l of a
 // fragment serves rows l / 4 and l / 4 + 8, whose tables are repeated for the four lanes of a

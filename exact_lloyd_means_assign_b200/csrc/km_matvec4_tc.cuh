@@ -7,8 +7,7 @@
 // straight to the row's TMEM lane (column c of a step holds codes 2c and 2c + 1), which is the
 // layout of a tensor-core row operand. Nothing is decoded twice whatever the number of tokens (up
 // to 32 per pass), and the only shared-memory traffic is the codes, one word per pair and the table
-// itself. (mma.sync m16n8k16 needs 32 cycles of a sub-partition's tensor pipe, more than the lookups
-// of its 256 weights take.)
+// itself. (The mma.sync form looks a pair up for every eight tokens.)
 //
 // Two half-tables of 64 rows x 256 entries (64 KB each) start on multiples of 64 KB of the shared
 // window, so that one byte permutation of (codes, row) is the address of a pair. The ring of
@@ -16,7 +15,7 @@
 // once lie in different banks, and the tokens' values. Steps are long because every hand-over
 // between the roles costs hundreds of cycles whatever it hands over.
 //
-// What it measured (16 tokens x 8192 x 8192 bf16, a scale per 64 weights, GPU time): 21 us, where the
+// What it measured (16 tokens x 8192 x 8192 bf16, a scale per 64 weights, GPU time): 21.6 us, where the
 // mma.sync form took 32; a step of 256 codes takes about 1040 cycles, of which the lookups are 640 and
 // the codes' bytes at full memory rate 700; some 6 us of the launch pass before the first step (codebooks read,
 // tables built) and after the last (the cluster's barriers). A single token is served by the mma.sync
@@ -338,8 +337,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (!ok) break;
             if (p.split > 1) {
-                // the parts of the cluster's blocks, in the first one's table space (one item per
-                // cluster then; at the barrier nobody needs a table any more)
+                // The parts of the cluster's blocks, in the first one's table space and, with 32 tokens and eight
+                // blocks, the first 4 KB of the ring above it (one item per cluster then; behind the barrier nobody
+                // needs a table any more, and every block's copies have landed and been used).
+                static_assert(kHalfTab + 8 * kTcRows * (NTOK + 1) * 4 <= kTcEnd, "parts of eight blocks");
                 const uint32_t mine = tab + (rank * kTcRows + row) * (NTOK + 1) * 4;
                 cluster_barrier();
                 uint32_t dst;

@@ -92,7 +92,7 @@ inline LossWs carve_loss(Carver &c, int64_t B, int64_t N, int64_t K, int64_t d, 
 
 // Gradients of rows of up to 128 16-bit values take the fused form (three tiles of S and one of O fill
 // TMEM; longer rows leave the exponentials the smaller part). 32768 points x 8192 rows at d = 128: dX
-// 146 us against 270 through P in memory, dC 149 against 268; 20000 x 300: dX 31 against 27, dC 31 against
+// 146 us against 270 through P in memory, dC 155 against 268; 20000 x 300: dX 31 against 27, dC 31 against
 // 36; 100000 x 64 at d = 32: dX 38 against 39, dC 48 against 50.
 inline bool fused_shape(km_dtype dt, int64_t d) { return dt != KM_F32 && d <= 128; }
 // Blocks of one gradient: all SMs, but two tiles at least for each.

@@ -16,7 +16,7 @@
 // beside the eight warps of exponentials. What each step gave (dX / dC of that case, us): one group
 // of warps in step 189 / 172; two groups with a buffer of S and P each 165 / 157; three buffers, one
 // thread issuing, and the loop over 32 columns rolled (the longer body displaced the issuer's
-// instructions) 146 / 149.
+// instructions) 146 / 149; draining O, and the look for infinite rows of the table, 146 / 155.
 //
 // A block's share is an equal run of the tiles of all row tiles, so that every SM works to the end; a row
 // tile that is shared by several blocks is summed from their partials, in block order.

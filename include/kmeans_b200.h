@@ -408,7 +408,7 @@ km_status km_matvec4(const void *x, km_dtype dtype, int64_t M, const uint8_t *pa
 
 /*
  * Table lookup (the decoding side of the assignment): Y[b,n,:] = scale * C[b, ids[b,n], :], zero
- * rows for ids outside [0,K). C[B,K,d] and Y[B,N,d] in `dtype`, the product rounded once. Values
+ * rows for ids outside [0,K). C[B,K,d] and Y[B,N,d] in `dtype`, the fp32 product rounded to it. Values
  * of rows that no id names are not read. Asynchronous on `stream`, no workspace.
  * Errors: KM_ERR_INVALID_ARG, KM_ERR_CUDA.
  */
@@ -423,8 +423,8 @@ km_status km_lookup(const void *C, km_dtype dtype, const int32_t *ids, int64_t B
  * rows of dY not read. Without accumulate, rows without tokens are set to zero; with it they are
  * left as they are. dY[B,N,d] in `dtype`; dC[B,K,d] in `out_dtype`, which is `dtype` or fp32.
  * ws: km_lookup_grad_workspace_size(...) bytes, 256-byte aligned (0 is returned for sizes that
- * are not provided); calls that may overlap need a workspace each. Asynchronous on `stream`. Errors: KM_ERR_INVALID_ARG; KM_ERR_UNSUPPORTED
- * (B*N or B*K of 2^31 or more, other out_dtype); KM_ERR_WORKSPACE; KM_ERR_CUDA.
+ * are not provided); calls that may overlap need a workspace each. Asynchronous on `stream`.
+ * Errors: KM_ERR_INVALID_ARG; KM_ERR_UNSUPPORTED (B*N or B*K of 2^31 or more, other out_dtype); KM_ERR_WORKSPACE; KM_ERR_CUDA.
  */
 size_t km_lookup_grad_workspace_size(int64_t B, int64_t N, int64_t K, int64_t d);
 km_status km_lookup_grad(const void *dY, km_dtype dtype, const int32_t *ids, int64_t B, int64_t N,
