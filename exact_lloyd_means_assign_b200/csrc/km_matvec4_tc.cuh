@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = true;
         for (int item = first; item < items; item += stride) {
             // everybody is done with the previous table; a warp that gave up takes all with it
+            __syncwarp();
             if (named_barrier_or(1, 32 * kTcDecode, !ok)) break;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
