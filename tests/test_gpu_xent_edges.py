@@ -248,3 +248,63 @@ def test_points_without_labels_of_other_forms_may_hold_anything(cuda_device, dty
         torch.cuda.synchronize()
         assert (loss[bad] == 0).all() and torch.isfinite(loss).all()
         assert torch.equal(dX, dX0) and torch.equal(dC, dC0)
+
+
+@pytest.mark.parametrize("N,K,d", [((1 << 25) + 3, 3, 64), ((1 << 24) + 5, 40, 136), (5, (1 << 24) + 5, 136), (70000, 70001, 8)])
+def test_sizes_beyond_32_bit_offsets(cuda_device, N, K, d):
+    # points or a table of more than 2^31 values, more than 2^32 logits; equal rows repeat with a period, so
+    # that the results are those of one period, and the last rows show the largest offsets
+    dtype, P = torch.bfloat16, 96
+    gen = torch.Generator(device=cuda_device).manual_seed(N % 1000)
+    x = torch.randn((min(N, P), d), generator=gen, device=cuda_device).to(dtype)
+    c = (torch.randn((min(K, P), d), generator=gen, device=cuda_device) * (2 / d ** 0.5)).to(dtype)
+    at_x, at_c = torch.arange(N, device=cuda_device) % x.shape[0], torch.arange(K, device=cuda_device) % c.shape[0]
+    X, C = x[at_x][None], c[at_c][None]
+    ids = (at_x % min(K, c.shape[0])).to(torch.int32)[None]
+    g = torch.full((1, N), 1.0 / N, device=cuda_device)
+    loss, lse = km.km_xent(X, C, ids)
+    dX, dC = km.km_xent_grad(X, C, ids, lse, g)
+    torch.cuda.synchronize()
+    assert km.km_device_error() == 0
+    # one period of points against the table's distinct rows, each as often as it stands there
+    times = torch.bincount(at_c, minlength=c.shape[0]).double()
+    z = x.double() @ c.double().t()
+    rs = torch.logsumexp(z + times.log(), 1)
+    t = ids[0, :x.shape[0]].long()
+    rl = rs - z.gather(1, t[:, None])[:, 0]
+    # (a logit's sum, the exponentials, and at most 320 additions of a tile's and the tiles' sums)
+    ez = ((d / 16 + 66) * 2.0 ** -23 * (x.double().abs() @ c.double().abs().t())).max()
+    els = ez + 2.0 ** -21 * (z.abs().max() + 2) + 320 * 2.0 ** -24 + 2.0 ** -23 * rs.abs().max()
+    assert (lse[0].double() - rs[at_x]).abs().max() <= els
+    assert (loss[0].double() - rl[at_x]).abs().max() <= els + ez + 2.0 ** -22 * (rs.abs().max() + z.abs().max())
+    p = torch.exp(z - rs[:, None])
+    rX = p @ (c.double() * times[:, None]) - c[t].double()
+    # (roundings of P and of the result, half a step each, in the norm of a period, first and last)
+    u = torch.finfo(dtype).eps / 2
+    for sl in (slice(0, x.shape[0]), slice(N - x.shape[0], N)):
+        ref = rX[at_x[sl]] / N
+        assert (dX[0, sl].double() - ref).norm() <= (2 * u + 2 * els + 2.0 ** -12) * ref.norm()
+    # dC of a row: all points' softmax parts, and its label's where it is the first of its kind
+    count = torch.bincount(at_x, minlength=x.shape[0]).double()
+    soft = (p * count[:, None]).t() @ x.double() / N
+    lab = torch.zeros_like(soft).index_add_(0, t, x.double() * count[:, None]) / N
+    mag = (p * count[:, None]).t() @ x.double().abs() / N + torch.zeros_like(soft).index_add_(0, t, x.double().abs() * count[:, None]) / N
+    for k in {0, min(K, c.shape[0]) - 1, K // 2, K - 1}:
+        ref = soft[at_c[k]] - (lab[at_c[k]] if k < c.shape[0] else 0)
+        tol = u * ref.abs() + (u + MAX_DRIFT + 2 * els + 2.0 ** -15) * mag[at_c[k]] + 1e-30
+        assert ((dC[0, k].double() - ref).abs() <= tol).all()
+
+
+def test_the_loss_over_very_many_table_rows(cuda_device):
+    # 2^24 table rows, alike by the dozen, so that the roundings of the tiles' sums would all point one way. What is
+    # left: 20 16-bit products to a logit, an exponential's 2^-21, 64 additions within a tile's half, ten of the joined sums
+    N, K, d = 4, (1 << 24) + 5, 16
+    gen = torch.Generator(device=cuda_device).manual_seed(3)
+    x = torch.randn((N, d), generator=gen, device=cuda_device).half()
+    c = (torch.randn((96, d), generator=gen, device=cuda_device) * 0.5).half()
+    at = torch.arange(K, device=cuda_device) % 96
+    _, lse = km.km_xent(x[None], c[at][None], torch.zeros((1, N), dtype=torch.int32, device=cuda_device))
+    z = x.double() @ c.double().t()
+    rs = torch.logsumexp(z + torch.bincount(at, minlength=96).double().log(), 1)
+    tol = 4 * 2.0 ** -23 * (x.double().abs() @ c.double().abs().t()).max() + 2.0 ** -21 + 80 * 2.0 ** -24 + 2.0 ** -23 * rs.max()
+    assert ((lse[0].double() - rs).abs() <= tol).all()
