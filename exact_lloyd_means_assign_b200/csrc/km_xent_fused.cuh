@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                 T *dst = static_cast<T *>(p.out) + (static_cast<int64_t>(b) * p.M + grow) * p.d + col;
                 float f[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(v[c][k]) * inv;
+                for (int k = 0; k < 32; ++k) f[k] = !COL && label < 0 ? 0.f : __uint_as_float(v[c][k]) * inv;
                 if (p.vec && col + 32 <= p.d) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -626,6 +626,8 @@ __global__ void __launch_bounds__(DN)
         for (int i = 1; i < PARTS; ++i) add(sums[i][col / 4]);
     }
     const float inv = rows ? rows[static_cast<int64_t>(r) * FR + row].factor : p_factor(wmax, pscale, true);
+    // (a row without a label is zero, whatever its zeros met in the table)
+    if (rows && rows[static_cast<int64_t>(r) * FR + row].label < 0) s = make_float4(0.f, 0.f, 0.f, 0.f);
     const float f[4] = {s.x * inv, s.y * inv, s.z * inv, s.w * inv};
 #pragma unroll
     for (int k = 0; k < 4; ++k)

@@ -142,6 +142,26 @@ def test_masked_table_rows(cuda_device, dtype, low, d, K, dead):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,K,d", [(150, 700, 64), (150, 90, 40), (2000, 5000, 128), (150, 700, 136), (9, 20000, 24)])
+def test_infinite_table_rows_stay_in_their_column(cuda_device, dtype, N, K, d):
+    # dX of a table with infinities is NaN in their column at most; elsewhere it is what finite masks give
+    X, C, ids, g = _inputs(1, N, K, d, dtype, cuda_device, seed=N + K)
+    X[..., -1] = 1
+    C[..., -1] = 0
+    dead = torch.arange(K, device=cuda_device) % 3 == 1
+    ids = (torch.arange(N, device=cuda_device, dtype=torch.int32) * 3 % (K - 2) // 3 * 3)[None].contiguous()
+    ids[0, ::5] = -1
+    got = {}
+    for low in (-3e4, -float("inf")):
+        C[:, dead, -1] = low
+        _, lse = km.km_xent(X, C, ids)
+        got[low] = km.km_xent_grad(X, C, ids, lse, g)
+    (x0, c0), (x1, c1) = got.values()
+    assert torch.equal(x0[..., :-1], x1[..., :-1]) and torch.equal(c0, c1)
+    assert (x1[0, ::5, :-1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("d", [64, 136])
 def test_every_row_masked(cuda_device, dtype, d):
     X, C, ids, _ = _inputs(1, 70, 400, d, dtype, cuda_device, seed=d)
